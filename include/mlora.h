@@ -482,6 +482,105 @@ MLORA_API mlora_status mlora_kv_write(const void *y, int M, int ld, int k_col, i
 MLORA_API mlora_status mlora_kv_commit(const int32_t *accepted, int B, int32_t *seq_len, mlora_stream stream);
 
 /* ------------------------------------------------------------------------- */
+/* The KV cache in 4 bits                                                     */
+/* ------------------------------------------------------------------------- */
+
+/* The same paged cache held in 4 bits (no counterpart on the pages, which ask
+ * for nothing past one cache for both passes): 4.5 bits a value instead of
+ * 16.  Each group of 16 values along a head's D has 16 E2M1 codes (one sign
+ * bit, two exponent bits, one mantissa bit: 0, .5, 1, 1.5, 2, 3, 4, 6) and one
+ * E4M3 scale (bias 7, largest finite 448); a value is code * scale * unit,
+ * `unit` one fp32 factor per cache that the caller fixes (1 unless the values
+ * lie outside what the scales reach: 2^-9 .. 448, times 6).
+ *   k_codes, v_codes    uint8 [num_blocks, H, block_size, D / 2]: two codes to
+ *                       a byte, the even element in the low half; 16-byte
+ *                       aligned;
+ *   k_scales, v_scales  uint8 [num_blocks, H, block_size, D / 16], E4M3;
+ *                       16-byte aligned.
+ * A page holds one head's tokens side by side, so that a pass over one head
+ * reads whole runs of memory.  block_table and seq_len are those of the bf16
+ * cache.
+ *
+ * mlora_kv_write_q4 takes the rows that mlora_kv_write takes (same arguments,
+ * positions, fallbacks and status bits) and quantises them as it writes.  For
+ * a group with largest magnitude amax, all in fp32 with IEEE division:
+ *   scale = E4M3(amax / (6 unit)),  code = E2M1(v / (scale unit)),
+ * both round to nearest even and saturating; a group whose scale is 0 gets
+ * codes 0; a group that holds a NaN gets the scale NaN and reads back as NaN.
+ * D % 16 == 0, num_blocks * H * block_size < 2^31, units finite and positive
+ * with 6 unit finite (MLORA_ERR_SHAPE / MLORA_ERR_ARG otherwise). */
+MLORA_API mlora_status mlora_kv_write_q4(const void *y, int M, int ld, int k_col, int v_col, int H, int D,
+                                         const int32_t *block_table, int B, int max_blocks, const int32_t *seq_len,
+                                         int rows_per_req, int t0, uint8_t *k_codes, uint8_t *k_scales,
+                                         uint8_t *v_codes, uint8_t *v_scales, float k_unit, float v_unit,
+                                         int num_blocks, int block_size, void *workspace, size_t ws_bytes,
+                                         mlora_stream stream);
+
+/* Read positions back as bf16 (one rounding of code * scale * unit, exact
+ * when unit is a power of two and nothing over- or underflows):
+ *   k_out, v_out  bf16 [B, rows, H, D] out: row (b, t) holds position
+ *                 start[b] + t where that is below end[b], else zeros;
+ *   start, end    int32 [B]; a negative start marks an unused request slot,
+ *                 whose rows are zeros.
+ * A position below end[b] whose slot lies outside the cache or the table
+ * reads as zeros and raises MLORA_DEV_BAD_SLOT.  B * rows < 2^31. */
+MLORA_API mlora_status mlora_kv_read_q4(const uint8_t *k_codes, const uint8_t *k_scales, const uint8_t *v_codes,
+                                        const uint8_t *v_scales, float k_unit, float v_unit, int H, int D,
+                                        const int32_t *block_table, int B, int max_blocks, const int32_t *start,
+                                        const int32_t *end, int rows, mlora_bf16 *k_out, mlora_bf16 *v_out,
+                                        int num_blocks, int block_size, void *workspace, size_t ws_bytes,
+                                        mlora_stream stream);
+
+/* ------------------------------------------------------------------------- */
+/* Attention over the cache                                                   */
+/* ------------------------------------------------------------------------- */
+
+/* The attention of a draft step, a verify pass or a prompt over the paged
+ * cache, after mlora_kv_write put the pass's own rows there.  Both passes of
+ * the InvisibleLoRA abstract read the one cache; the pages give no formula, so
+ * this is the usual one:
+ *   o[m, h] = sum_j p_j v_j,  p = softmax over j of  scale * q[m, h] . k_j,
+ * over the positions j that row m sees.  Row m is request b = m / rows_per_req
+ * at step t = m % rows_per_req and position p = seq_len[b] + t0 + t; it sees
+ * j <= p, and with window > 0 of those only j > p - window (the last `window`
+ * positions, its own among them) and j < sinks (the first tokens, which stay
+ * visible).  Query head h reads cache head h / (Hq / H).
+ *   y       bf16 [M, ld]: the fused q|k|v output; q of row m is
+ *           y[m, q_col : q_col + Hq*D], Hq heads of D;
+ *   out     bf16 [M, Hq*D] out, 16-byte aligned;
+ *   k_cache, v_cache, block_table, seq_len, rows_per_req, t0: as
+ *           mlora_kv_write.
+ * Scores, the softmax's statistics and the sums are fp32; the softmax's
+ * weights enter the second product rounded to the product's input type (bf16
+ * over the bf16 cache, fp16 over the 4-bit one), and the output is rounded
+ * once.  A position whose slot lies outside the cache or the table is not
+ * seen (MLORA_DEV_BAD_SLOT).  A row that sees nothing, and every row of an
+ * unused request slot (negative seq_len), is zeros.  What a row does not see
+ * has no effect on it, whatever it holds (infinities and NaN too).  Results do
+ * not depend on how the work was split over time: the same inputs give the
+ * same bits.
+ *   Hq % H == 0, D % 16 == 0, D <= 256, Hq * D <= 2^20, window >= 0,
+ *   sinks >= 0, num_blocks * block_size < 2^31 (times H over the 4-bit cache),
+ *   scale finite.  Heads of 64 and 128 with 16-byte aligned rows (y, caches,
+ *   ld and q_col multiples of 8) run on the tensor cores; anything else on a
+ *   slower kernel.  Workspace: mlora_attention_workspace_bytes. */
+MLORA_API size_t mlora_attention_workspace_bytes(int M, int rows_per_req, int Hq, int H, int D);
+MLORA_API mlora_status mlora_attention(const void *y, int M, int ld, int q_col, int Hq, int H, int D,
+                                       const void *k_cache, const void *v_cache, int num_blocks, int block_size,
+                                       const int32_t *block_table, int B, int max_blocks, const int32_t *seq_len,
+                                       int rows_per_req, int t0, int window, int sinks, float scale, mlora_bf16 *out,
+                                       void *workspace, size_t ws_bytes, mlora_stream stream);
+
+/* The same over the 4-bit cache (mlora_kv_write_q4). */
+MLORA_API mlora_status mlora_attention_q4(const void *y, int M, int ld, int q_col, int Hq, int H, int D,
+                                          const uint8_t *k_codes, const uint8_t *k_scales, const uint8_t *v_codes,
+                                          const uint8_t *v_scales, float k_unit, float v_unit, int num_blocks,
+                                          int block_size, const int32_t *block_table, int B, int max_blocks,
+                                          const int32_t *seq_len, int rows_per_req, int t0, int window, int sinks,
+                                          float scale, mlora_bf16 *out, void *workspace, size_t ws_bytes,
+                                          mlora_stream stream);
+
+/* ------------------------------------------------------------------------- */
 /* Run-time draft gate (host functions; no GPU needed)                        */
 /* ------------------------------------------------------------------------- */
 

@@ -12,6 +12,8 @@ device is not compute capability 10.3, the calls raise.
     verify_accept_logits(z_p, z_q, draft_tok, uniforms)                  the same on logits (softmax fused)
     softmax(z), draft_sample(z_q, uniforms)                              logits -> probabilities; draft draw
     kv_write(y, ...), kv_commit(accepted, seq_len)                       hybrid KV cache (paged)
+    kv_write_q4(y, ...), kv_read_q4(...)                                  the same cache held in 4 bits
+    attention(y, ...), attention_q4(y, ...)                              attention over either cache
     quantize_rows_fp8(W), linear_fp8(x, W8, w_scale)                     draft pass on E4M3 weights
     plan_segments(...), shrink(...)                                      steps a1, a2 alone
 
@@ -96,6 +98,19 @@ _SIGNATURES = {
     "mlora_kv_write": (_c_int, [_c_ptr, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _c_ptr, _c_int, _c_int,
                                 _c_ptr, _c_int, _c_int, _c_ptr, _c_ptr, _c_int, _c_int, _c_ptr, _c_size, _c_ptr]),
     "mlora_kv_commit": (_c_int, [_c_ptr, _c_int, _c_ptr, _c_ptr]),
+    "mlora_kv_write_q4": (_c_int, [_c_ptr, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _c_ptr, _c_int, _c_int,
+                                   _c_ptr, _c_int, _c_int, _c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_float, _c_float, _c_int,
+                                   _c_int, _c_ptr, _c_size, _c_ptr]),
+    "mlora_kv_read_q4": (_c_int, [_c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_float, _c_float, _c_int, _c_int, _c_ptr, _c_int,
+                                  _c_int, _c_ptr, _c_ptr, _c_int, _c_ptr, _c_ptr, _c_int, _c_int, _c_ptr, _c_size,
+                                  _c_ptr]),
+    "mlora_attention_workspace_bytes": (_c_size, [_c_int, _c_int, _c_int, _c_int, _c_int]),
+    "mlora_attention": (_c_int, [_c_ptr, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _c_ptr, _c_ptr, _c_int, _c_int,
+                                 _c_ptr, _c_int, _c_int, _c_ptr, _c_int, _c_int, _c_int, _c_int, _c_float, _c_ptr,
+                                 _c_ptr, _c_size, _c_ptr]),
+    "mlora_attention_q4": (_c_int, [_c_ptr, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _c_ptr, _c_ptr, _c_ptr,
+                                    _c_ptr, _c_float, _c_float, _c_int, _c_int, _c_ptr, _c_int, _c_int, _c_ptr, _c_int,
+                                    _c_int, _c_int, _c_int, _c_float, _c_ptr, _c_ptr, _c_size, _c_ptr]),
     "mlora_status_string": (ctypes.c_char_p, [_c_int]),
     "mlora_device_supported": (_c_int, []),
     "mlora_launch_count": (ctypes.c_uint64, []),
@@ -481,6 +496,136 @@ def kv_commit(accepted: torch.Tensor, seq_len: torch.Tensor, stream=None) -> tor
                                  _stream(stream))
     _check(st, "kv_commit")
     return seq_len
+
+
+def _q4_cache(k_codes, k_scales, v_codes, v_scales):
+    """Shape checks of a 4-bit cache: (num_blocks, H, block_size, D) and the four pointers."""
+    nb, H, bs, half = k_codes.shape
+    D = 2 * half
+    if tuple(v_codes.shape) != (nb, H, bs, half) or D % 16 != 0:
+        raise ValueError("k_codes and v_codes must both be [num_blocks, H, block_size, D/2], D a multiple of 16")
+    if tuple(k_scales.shape) != (nb, H, bs, D // 16) or tuple(v_scales.shape) != (nb, H, bs, D // 16):
+        raise ValueError("k_scales and v_scales must both be [num_blocks, H, block_size, D/16]")
+    return nb, H, bs, D, [_need(t, n, torch.uint8, 4) for t, n in ((k_codes, "k_codes"), (k_scales, "k_scales"),
+                                                                   (v_codes, "v_codes"), (v_scales, "v_scales"))]
+
+
+def kv_write_q4(y: torch.Tensor, k_col: int, v_col: int, H: int, D: int, block_table: torch.Tensor,
+                seq_len: torch.Tensor, rows_per_req: int, t0: int, k_codes: torch.Tensor, k_scales: torch.Tensor,
+                v_codes: torch.Tensor, v_scales: torch.Tensor, k_unit: float = 1.0, v_unit: float = 1.0,
+                ws: Workspace = None, stream=None):
+    """kv_write into the cache held in 4 bits: codes uint8 [num_blocks, H,
+    block_size, D/2] and E4M3 scales uint8 [num_blocks, H, block_size, D/16]
+    (one per 16 values); a value is code * scale * unit.  Returns the cache."""
+    M, ld = y.shape
+    B, max_blocks = block_table.shape
+    nb, H2, bs, D2, ptrs = _q4_cache(k_codes, k_scales, v_codes, v_scales)
+    if (H2, D2) != (H, D):
+        raise ValueError("the cache's heads disagree with H and D")
+    if seq_len.numel() != B:
+        raise ValueError("seq_len must have one entry per block-table row")
+    if ws is None:
+        ws = Workspace(kv_workspace_bytes(), device=y.device, stream=stream)
+    st = _load().mlora_kv_write_q4(_need(y, "y", torch.bfloat16, 2), M, ld, int(k_col), int(v_col), int(H), int(D),
+                                   _need(block_table, "block_table", torch.int32, 2), B, max_blocks,
+                                   _need(seq_len, "seq_len", torch.int32, 1), int(rows_per_req), int(t0), *ptrs,
+                                   float(k_unit), float(v_unit), nb, bs, ws.ptr, ws.nbytes, _stream(stream))
+    _check(st, "kv_write_q4")
+    return k_codes, k_scales, v_codes, v_scales
+
+
+def kv_read_q4(k_codes: torch.Tensor, k_scales: torch.Tensor, v_codes: torch.Tensor, v_scales: torch.Tensor,
+               block_table: torch.Tensor, start: torch.Tensor, end: torch.Tensor, rows: int, k_unit: float = 1.0,
+               v_unit: float = 1.0, ws: Workspace = None, k: torch.Tensor = None, v: torch.Tensor = None, stream=None):
+    """Positions start[b] .. start[b] + rows - 1 of every request's 4-bit cache
+    as bf16 [B, rows, H, D] (K, V); zeros from end[b] on."""
+    B, max_blocks = block_table.shape
+    nb, H, bs, D, ptrs = _q4_cache(k_codes, k_scales, v_codes, v_scales)
+    if start.numel() != B or end.numel() != B:
+        raise ValueError("start and end must have one entry per block-table row")
+    if rows < 0:
+        raise ValueError("rows must not be negative")
+    if ws is None:
+        ws = Workspace(kv_workspace_bytes(), device=k_codes.device, stream=stream)
+    if k is None:
+        k = torch.empty((B, rows, H, D), dtype=torch.bfloat16, device=k_codes.device)
+    if v is None:
+        v = torch.empty((B, rows, H, D), dtype=torch.bfloat16, device=k_codes.device)
+    if tuple(k.shape) != (B, rows, H, D) or tuple(v.shape) != (B, rows, H, D):
+        raise ValueError("k and v must be [B, rows, H, D]")
+    st = _load().mlora_kv_read_q4(*ptrs, float(k_unit), float(v_unit), H, D,
+                                  _need(block_table, "block_table", torch.int32, 2), B, max_blocks,
+                                  _need(start, "start", torch.int32, 1), _need(end, "end", torch.int32, 1), int(rows),
+                                  _need(k, "k", torch.bfloat16, 4), _need(v, "v", torch.bfloat16, 4), nb, bs, ws.ptr,
+                                  ws.nbytes, _stream(stream))
+    _check(st, "kv_read_q4")
+    return k, v
+
+
+def attention_workspace_bytes(M: int, rows_per_req: int, Hq: int, H: int, D: int) -> int:
+    return int(_load().mlora_attention_workspace_bytes(M, rows_per_req, Hq, H, D))
+
+
+def _attention_common(y, q_col, Hq, H, D, block_table, seq_len, rows_per_req, scale, ws, out, stream):
+    M = y.shape[0]
+    if seq_len.numel() != block_table.shape[0]:
+        raise ValueError("seq_len must have one entry per block-table row")
+    if scale is None:
+        scale = D ** -0.5
+    if ws is None:
+        ws = Workspace(attention_workspace_bytes(M, rows_per_req, Hq, H, D), device=y.device, stream=stream)
+    if out is None:
+        out = torch.empty((M, Hq * D), dtype=torch.bfloat16, device=y.device)
+    if tuple(out.shape) != (M, Hq * D):
+        raise ValueError("out must be [M, Hq * D]")
+    return float(scale), ws, out
+
+
+def attention(y: torch.Tensor, q_col: int, Hq: int, k_cache: torch.Tensor, v_cache: torch.Tensor,
+              block_table: torch.Tensor, seq_len: torch.Tensor, rows_per_req: int, t0: int, scale: float = None,
+              window: int = 0, sinks: int = 0, ws: Workspace = None, out: torch.Tensor = None,
+              stream=None) -> torch.Tensor:
+    """Attention of one pass's rows over the paged cache kv_write fills.
+
+    q of row m is y[m, q_col : q_col + Hq*D]; the row is request
+    m // rows_per_req at position seq_len[b] + t0 + m % rows_per_req and sees
+    the positions up to its own; with window > 0 only the last `window` of them
+    and the first `sinks`.  scale defaults to D ** -0.5.  Returns bf16 [M, Hq*D]."""
+    M, ld = y.shape
+    B, max_blocks = block_table.shape
+    nb, bs, H, D = k_cache.shape
+    if tuple(v_cache.shape) != (nb, bs, H, D):
+        raise ValueError("k_cache and v_cache must both be [num_blocks, block_size, H, D]")
+    scale, ws, out = _attention_common(y, q_col, Hq, H, D, block_table, seq_len, rows_per_req, scale, ws, out, stream)
+    st = _load().mlora_attention(_need(y, "y", torch.bfloat16, 2), M, ld, int(q_col), int(Hq), H, D,
+                                 _need(k_cache, "k_cache", torch.bfloat16, 4),
+                                 _need(v_cache, "v_cache", torch.bfloat16, 4), nb, bs,
+                                 _need(block_table, "block_table", torch.int32, 2), B, max_blocks,
+                                 _need(seq_len, "seq_len", torch.int32, 1), int(rows_per_req), int(t0), int(window),
+                                 int(sinks), scale, _need(out, "out", torch.bfloat16, 2), ws.ptr, ws.nbytes,
+                                 _stream(stream))
+    _check(st, "attention")
+    return out
+
+
+def attention_q4(y: torch.Tensor, q_col: int, Hq: int, k_codes: torch.Tensor, k_scales: torch.Tensor,
+                 v_codes: torch.Tensor, v_scales: torch.Tensor, block_table: torch.Tensor, seq_len: torch.Tensor,
+                 rows_per_req: int, t0: int, scale: float = None, window: int = 0, sinks: int = 0,
+                 k_unit: float = 1.0, v_unit: float = 1.0, ws: Workspace = None, out: torch.Tensor = None,
+                 stream=None) -> torch.Tensor:
+    """attention over the cache that kv_write_q4 fills."""
+    M, ld = y.shape
+    B, max_blocks = block_table.shape
+    nb, H, bs, D, ptrs = _q4_cache(k_codes, k_scales, v_codes, v_scales)
+    scale, ws, out = _attention_common(y, q_col, Hq, H, D, block_table, seq_len, rows_per_req, scale, ws, out, stream)
+    st = _load().mlora_attention_q4(_need(y, "y", torch.bfloat16, 2), M, ld, int(q_col), int(Hq), H, D, *ptrs,
+                                    float(k_unit), float(v_unit), nb, bs,
+                                    _need(block_table, "block_table", torch.int32, 2), B, max_blocks,
+                                    _need(seq_len, "seq_len", torch.int32, 1), int(rows_per_req), int(t0),
+                                    int(window), int(sinks), scale, _need(out, "out", torch.bfloat16, 2), ws.ptr,
+                                    ws.nbytes, _stream(stream))
+    _check(st, "attention_q4")
+    return out
 
 
 def draft_gate(t_cycle: dict, t_plain: float, alpha: float):

@@ -2,6 +2,8 @@
 // Nothing here computes a result; every step runs in the CUDA kernels.
 #include <algorithm>
 #include <atomic>
+#include <cfloat>
+#include <cmath>
 #include <cstring>
 
 #include "common.cuh"
@@ -577,6 +579,170 @@ mlora_status mlora_kv_commit(const int32_t *accepted, int B, int32_t *seq_len, m
   if (B < 1 || B > MLORA_MAX_ROWS) return MLORA_ERR_SHAPE;
   if (!accepted || !seq_len) return MLORA_ERR_ARG;
   return cuda_status(launch_kv_commit(accepted, B, seq_len, (cudaStream_t)stream));
+}
+
+// Sizes of a 4-bit cache: slots of one head, (block, head, offset), are
+// indexed with 32 bits.
+static bool kv4_sizes_ok(int H, int D, int B, int max_blocks, int num_blocks, int block_size) {
+  return H >= 1 && D >= 16 && D % 16 == 0 && (long long)H * D <= (1 << 20) && B >= 1 && B <= MLORA_MAX_ROWS &&
+         max_blocks >= 1 && num_blocks >= 1 && block_size >= 1 &&
+         (long long)num_blocks * block_size <= INT32_MAX / H;
+}
+static bool unit_ok(float u) { return u > 0.f && u * 6.f <= FLT_MAX; }
+static bool aligned4(const void *a, const void *b, const void *c, const void *d) {
+  return aligned(a, 16) && aligned(b, 16) && aligned(c, 16) && aligned(d, 16);
+}
+
+static Kv4 kv4_of(const uint8_t *kc, const uint8_t *ks, const uint8_t *vc, const uint8_t *vs, float ku, float vu, int H,
+                  int D, const int32_t *block_table, int B, int max_blocks, int num_blocks, int block_size,
+                  void *workspace) {
+  Kv4 c;
+  c.codes[0] = const_cast<uint8_t *>(kc);
+  c.codes[1] = const_cast<uint8_t *>(vc);
+  c.scales[0] = const_cast<uint8_t *>(ks);
+  c.scales[1] = const_cast<uint8_t *>(vs);
+  c.unit[0] = ku;
+  c.unit[1] = vu;
+  c.H = H;
+  c.D = D;
+  c.num_blocks = num_blocks;
+  c.block_size = block_size;
+  c.block_table = block_table;
+  c.B = B;
+  c.max_blocks = max_blocks;
+  c.status = reinterpret_cast<uint32_t *>((uint8_t *)workspace + WS_STATUS_OFF);
+  return c;
+}
+
+mlora_status mlora_kv_write_q4(const void *y, int M, int ld, int k_col, int v_col, int H, int D,
+                               const int32_t *block_table, int B, int max_blocks, const int32_t *seq_len,
+                               int rows_per_req, int t0, uint8_t *k_codes, uint8_t *k_scales, uint8_t *v_codes,
+                               uint8_t *v_scales, float k_unit, float v_unit, int num_blocks, int block_size,
+                               void *workspace, size_t ws_bytes, mlora_stream stream) {
+  if (!kv4_sizes_ok(H, D, B, max_blocks, num_blocks, block_size) || M < 0 || M > MLORA_MAX_ROWS || rows_per_req < 1 ||
+      (long long)M > (long long)B * rows_per_req || t0 < 0 || k_col < 0 || v_col < 0 ||
+      (long long)k_col + (long long)H * D > ld || (long long)v_col + (long long)H * D > ld)
+    return MLORA_ERR_SHAPE;
+  if ((M > 0 && !y) || !block_table || !seq_len || !k_codes || !k_scales || !v_codes || !v_scales)
+    return MLORA_ERR_ARG;  // y may be empty
+  if (!unit_ok(k_unit) || !unit_ok(v_unit) || !aligned4(k_codes, k_scales, v_codes, v_scales)) return MLORA_ERR_ARG;
+  if (!workspace || !aligned(workspace, 256) || ws_bytes < mlora_kv_workspace_bytes()) return MLORA_ERR_WORKSPACE;
+  const int sms = device_sms();
+  if (sms <= 0) return MLORA_ERR_CUDA;
+  Kv4Write a;
+  a.c = kv4_of(k_codes, k_scales, v_codes, v_scales, k_unit, v_unit, H, D, block_table, B, max_blocks, num_blocks,
+               block_size, workspace);
+  a.y = (const uint16_t *)y;
+  a.M = M;
+  a.ld = ld;
+  a.col[0] = k_col;
+  a.col[1] = v_col;
+  a.seq_len = seq_len;
+  a.rows_per_req = rows_per_req;
+  a.t0 = t0;
+  return cuda_status(launch_kv_write_q4(a, sms, (cudaStream_t)stream));
+}
+
+mlora_status mlora_kv_read_q4(const uint8_t *k_codes, const uint8_t *k_scales, const uint8_t *v_codes,
+                              const uint8_t *v_scales, float k_unit, float v_unit, int H, int D,
+                              const int32_t *block_table, int B, int max_blocks, const int32_t *start,
+                              const int32_t *end, int rows, mlora_bf16 *k_out, mlora_bf16 *v_out, int num_blocks,
+                              int block_size, void *workspace, size_t ws_bytes, mlora_stream stream) {
+  if (!kv4_sizes_ok(H, D, B, max_blocks, num_blocks, block_size) || rows < 0 || (long long)B * rows > INT32_MAX)
+    return MLORA_ERR_SHAPE;
+  if (!block_table || !start || !end || !k_codes || !k_scales || !v_codes || !v_scales ||
+      (rows > 0 && (!k_out || !v_out)))
+    return MLORA_ERR_ARG;
+  if (!unit_ok(k_unit) || !unit_ok(v_unit) || !aligned4(k_codes, k_scales, v_codes, v_scales) ||
+      !aligned(k_out, 16) || !aligned(v_out, 16))
+    return MLORA_ERR_ARG;
+  if (!workspace || !aligned(workspace, 256) || ws_bytes < mlora_kv_workspace_bytes()) return MLORA_ERR_WORKSPACE;
+  const int sms = device_sms();
+  if (sms <= 0) return MLORA_ERR_CUDA;
+  Kv4Read a;
+  a.c = kv4_of(k_codes, k_scales, v_codes, v_scales, k_unit, v_unit, H, D, block_table, B, max_blocks, num_blocks,
+               block_size, workspace);
+  a.start = start;
+  a.end = end;
+  a.rows = rows;
+  a.out[0] = (uint16_t *)k_out;
+  a.out[1] = (uint16_t *)v_out;
+  return cuda_status(launch_kv_read_q4(a, sms, (cudaStream_t)stream));
+}
+
+static bool attn_heads_ok(int M, int rows_per_req, int Hq, int H, int D) {
+  return M >= 0 && M <= MLORA_MAX_ROWS && rows_per_req >= 1 && H >= 1 && Hq >= H && Hq % H == 0 && D >= 16 &&
+         D % 16 == 0 && D <= 256 && (long long)Hq * D <= (1 << 20);
+}
+
+size_t mlora_attention_workspace_bytes(int M, int rows_per_req, int Hq, int H, int D) {
+  if (!attn_heads_ok(M, rows_per_req, Hq, H, D)) return 0;
+  return WS_INIT_BYTES;
+}
+
+static mlora_status attention_impl(const void *y, int M, int ld, int q_col, int Hq, int H, int D, const void *k,
+                                   const void *v, const uint8_t *ks, const uint8_t *vs, float k_unit, float v_unit,
+                                   int num_blocks, int block_size, const int32_t *block_table, int B, int max_blocks,
+                                   const int32_t *seq_len, int rows_per_req, int t0, int window, int sinks, float scale,
+                                   mlora_bf16 *out, void *workspace, size_t ws_bytes, mlora_stream stream, bool q4) {
+  if (!attn_heads_ok(M, rows_per_req, Hq, H, D) || B < 1 || B > MLORA_MAX_ROWS ||
+      (long long)M > (long long)B * rows_per_req || t0 < 0 || window < 0 || sinks < 0 || max_blocks < 1 ||
+      num_blocks < 1 || block_size < 1 || (long long)num_blocks * block_size > INT32_MAX / (q4 ? H : 1) || q_col < 0 ||
+      (long long)q_col + (long long)Hq * D > ld)
+    return MLORA_ERR_SHAPE;
+  if ((M > 0 && (!y || !out)) || !k || !v || !block_table || !seq_len || !isfinite(scale) || !aligned(out, 16))
+    return MLORA_ERR_ARG;
+  if (q4 && (!ks || !vs || !aligned4(k, ks, v, vs) || !unit_ok(k_unit) || !unit_ok(v_unit))) return MLORA_ERR_ARG;
+  if (!workspace || !aligned(workspace, 256) || ws_bytes < mlora_attention_workspace_bytes(M, rows_per_req, Hq, H, D))
+    return MLORA_ERR_WORKSPACE;
+  const int sms = device_sms();
+  if (sms <= 0) return MLORA_ERR_CUDA;
+  AttnArgs a;
+  a.y = (const uint16_t *)y;
+  a.ld = ld;
+  a.q_col = q_col;
+  a.M = M;
+  a.Hq = Hq;
+  a.H = H;
+  a.D = D;
+  a.k = k;
+  a.v = v;
+  a.ks = ks;
+  a.vs = vs;
+  a.num_blocks = num_blocks;
+  a.block_size = block_size;
+  a.block_table = block_table;
+  a.B = B;
+  a.max_blocks = max_blocks;
+  a.seq_len = seq_len;
+  a.rows_per_req = rows_per_req;
+  a.t0 = t0;
+  a.window = window;
+  a.sinks = sinks;
+  a.scale_log2 = (float)((double)scale * k_unit * 1.4426950408889634);
+  a.v_unit = v_unit;
+  a.out = (uint16_t *)out;
+  a.status = reinterpret_cast<uint32_t *>((uint8_t *)workspace + WS_STATUS_OFF);
+  return cuda_status(launch_attention(a, q4, sms, (cudaStream_t)stream));
+}
+
+mlora_status mlora_attention(const void *y, int M, int ld, int q_col, int Hq, int H, int D, const void *k_cache,
+                             const void *v_cache, int num_blocks, int block_size, const int32_t *block_table, int B,
+                             int max_blocks, const int32_t *seq_len, int rows_per_req, int t0, int window, int sinks,
+                             float scale, mlora_bf16 *out, void *workspace, size_t ws_bytes, mlora_stream stream) {
+  return attention_impl(y, M, ld, q_col, Hq, H, D, k_cache, v_cache, nullptr, nullptr, 1.f, 1.f, num_blocks, block_size,
+                        block_table, B, max_blocks, seq_len, rows_per_req, t0, window, sinks, scale, out, workspace,
+                        ws_bytes, stream, false);
+}
+
+mlora_status mlora_attention_q4(const void *y, int M, int ld, int q_col, int Hq, int H, int D, const uint8_t *k_codes,
+                                const uint8_t *k_scales, const uint8_t *v_codes, const uint8_t *v_scales, float k_unit,
+                                float v_unit, int num_blocks, int block_size, const int32_t *block_table, int B,
+                                int max_blocks, const int32_t *seq_len, int rows_per_req, int t0, int window, int sinks,
+                                float scale, mlora_bf16 *out, void *workspace, size_t ws_bytes, mlora_stream stream) {
+  return attention_impl(y, M, ld, q_col, Hq, H, D, k_codes, v_codes, k_scales, v_scales, k_unit, v_unit, num_blocks,
+                        block_size, block_table, B, max_blocks, seq_len, rows_per_req, t0, window, sinks, scale, out,
+                        workspace, ws_bytes, stream, true);
 }
 
 double mlora_expected_tokens(double alpha, int k) {

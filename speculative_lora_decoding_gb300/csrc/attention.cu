@@ -1,0 +1,126 @@
+// Attention over the paged KV cache, bf16 or 4-bit (include/mlora.h): the
+// rows of a draft step, a verify pass or a prompt against the positions each
+// of them sees.
+//
+//   o = sum_j 2^(s_j - m) v_j / sum_j 2^(s_j - m),   s_j = scale log2(e) q . k_j
+//
+// in one pass over the positions with a running maximum m: when m grows to m',
+// the sums so far are multiplied by 2^(m - m').
+#include "common.cuh"
+#include "e2m1.cuh"
+#include "launch.h"
+#include "prob.cuh"
+
+namespace mlora {
+
+constexpr float NEG_INF = -__builtin_huge_valf();
+
+// ---------------------------------------------------------------------------
+// Any head size up to 256 and any alignment: one CTA per (row, query head),
+// its four warps take every fourth position, a lane holds elements lane +
+// 32 i of the head.  Latency bound; the tensor-core kernels take the usual
+// heads.
+// ---------------------------------------------------------------------------
+constexpr int AG_WARPS = 4;
+constexpr int AG_VALS = 8;  // D <= 256
+
+template <bool Q4>
+__device__ __forceinline__ float cache_value(const void *p, const uint8_t *scales, size_t row, int D, int e) {
+  if (!Q4) return bf16_bits_to_float(__ldg(static_cast<const uint16_t *>(p) + row * D + e));
+  const uint32_t byte = __ldg(static_cast<const uint8_t *>(p) + row * (D / 2) + e / 2);
+  uint32_t f[4];
+  e2m1x8_to_f16(e & 1 ? byte >> 4 : byte & 15u, f);
+  return f16_lo(f[0]) * e4m3_to_float(__ldg(scales + row * (D / Q4_GROUP) + e / Q4_GROUP));
+}
+
+template <bool Q4>
+__global__ void __launch_bounds__(32 * AG_WARPS) attn_general_kernel(const AttnArgs a) {
+  __shared__ float so[AG_WARPS][256], sm[AG_WARPS], sl[AG_WARPS];
+  grid_launch_dependents();
+  grid_dependency_wait();  // y and the cache come from the kernels just before
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int D = a.D, G = a.Hq / a.H;
+  for (long long item = blockIdx.x; item < (long long)a.M * a.Hq; item += gridDim.x) {
+    const int m = (int)(item / a.Hq), hq = (int)(item - (long long)m * a.Hq), h = hq / G;
+    const int b = m / a.rows_per_req, t = m - b * a.rows_per_req;
+    const int L = a.seq_len[b];
+    float q[AG_VALS], o[AG_VALS];
+    float mx = NEG_INF, l = 0.f;
+#pragma unroll
+    for (int i = 0; i < AG_VALS; ++i) {
+      const int e = lane + 32 * i;
+      q[i] = e < D ? bf16_bits_to_float(a.y[(size_t)m * a.ld + a.q_col + (size_t)hq * D + e]) * a.scale_log2 : 0.f;
+      o[i] = 0.f;
+    }
+    if (L >= 0) {
+      const long long pos = (long long)L + a.t0 + t;
+      const long long extent = (long long)a.max_blocks * a.block_size;
+      const long long first = a.window && pos >= a.window ? pos - a.window + 1 : 0;  // of the window
+      const long long sink = first < a.sinks ? first : a.sinks;
+      if (pos >= extent && threadIdx.x == 0) raise_status(a.status, MLORA_DEV_BAD_SLOT);
+      const long long n = sink + (pos - first + 1);
+      for (long long i = warp; i < n; i += AG_WARPS) {
+        const long long j = i < sink ? i : first + (i - sink);
+        if (j >= extent) break;
+        const int page = (int)(j / a.block_size), off = (int)(j - (long long)page * a.block_size);
+        const int blk = a.block_table[(size_t)b * a.max_blocks + page];
+        if (blk < 0 || blk >= a.num_blocks) {
+          if (lane == 0) raise_status(a.status, MLORA_DEV_BAD_SLOT);
+          continue;
+        }
+        const size_t row = Q4 ? ((size_t)blk * a.H + h) * a.block_size + off
+                              : ((size_t)blk * a.block_size + off) * a.H + h;
+        float s = 0.f;
+#pragma unroll
+        for (int i2 = 0; i2 < AG_VALS; ++i2) {
+          const int e = lane + 32 * i2;
+          if (e < D) s += q[i2] * cache_value<Q4>(a.k, a.ks, row, D, e);
+        }
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
+        if (s == NEG_INF) continue;  // weight 0
+        const float mn = fmaxf(mx, s);
+        const float corr = exp2_hw(mx - mn), p = exp2_hw(s - mn);
+        mx = mn;
+        l = l * corr + p;
+#pragma unroll
+        for (int i2 = 0; i2 < AG_VALS; ++i2) {
+          const int e = lane + 32 * i2;
+          if (e < D) o[i2] = o[i2] * corr + p * cache_value<Q4>(a.v, a.vs, row, D, e);
+        }
+      }
+    }
+    if (lane == 0) {
+      sm[warp] = mx;
+      sl[warp] = l;
+    }
+#pragma unroll
+    for (int i = 0; i < AG_VALS; ++i) so[warp][lane + 32 * i] = o[i];
+    __syncthreads();
+    float M4 = NEG_INF, lt = 0.f, w[AG_WARPS];
+#pragma unroll
+    for (int k = 0; k < AG_WARPS; ++k) M4 = fmaxf(M4, sm[k]);
+#pragma unroll
+    for (int k = 0; k < AG_WARPS; ++k) {
+      w[k] = sl[k] != 0.f ? exp2_hw(sm[k] - M4) : 0.f;  // a warp that saw nothing (l = 0) has no part
+      lt += sl[k] * w[k];
+    }
+    for (int e = threadIdx.x; e < D; e += 32 * AG_WARPS) {
+      float v = 0.f;
+#pragma unroll
+      for (int k = 0; k < AG_WARPS; ++k) v += so[k][e] * w[k];
+      a.out[((size_t)m * a.Hq + hq) * D + e] = float_to_bf16_bits(lt != 0.f ? v * a.v_unit / lt : 0.f);
+    }
+    __syncthreads();  // the scratch is used again
+  }
+}
+
+cudaError_t launch_attention(const AttnArgs &a, bool q4, int num_sms, cudaStream_t s) {
+  if (a.M <= 0) return cudaSuccess;
+  const long long items = (long long)a.M * a.Hq;
+  const unsigned grid = (unsigned)(items < (1 << 22) ? items : (1 << 22));
+  if (q4) return launch_pdl(attn_general_kernel<true>, dim3(grid), dim3(32 * AG_WARPS), 0, s, a);
+  return launch_pdl(attn_general_kernel<false>, dim3(grid), dim3(32 * AG_WARPS), 0, s, a);
+}
+
+}  // namespace mlora

@@ -175,4 +175,51 @@ struct KvWrite {
 cudaError_t launch_kv_write(const KvWrite &a, int num_sms, cudaStream_t s);
 cudaError_t launch_kv_commit(const int32_t *accepted, int B, int32_t *seq_len, cudaStream_t s);
 
+// The KV cache in 4 bits (kvq4.cu): codes [num_blocks, H, block_size, D/2],
+// scales [num_blocks, H, block_size, D/16].
+struct Kv4 {
+  uint8_t *codes[2], *scales[2];  // K, V
+  float unit[2];
+  int H, D, num_blocks, block_size;
+  const int32_t *block_table;
+  int B, max_blocks;
+  uint32_t *status;
+};
+struct Kv4Write {
+  Kv4 c;
+  const uint16_t *y;
+  int M, ld, col[2];
+  const int32_t *seq_len;
+  int rows_per_req, t0;
+};
+struct Kv4Read {
+  Kv4 c;
+  const int32_t *start, *end;
+  int rows;
+  uint16_t *out[2];
+};
+cudaError_t launch_kv_write_q4(const Kv4Write &a, int num_sms, cudaStream_t s);
+cudaError_t launch_kv_read_q4(const Kv4Read &a, int num_sms, cudaStream_t s);
+
+// Attention over the paged cache (attention.cu).  k and v are the bf16 caches
+// [num_blocks, block_size, H, D], or with q4 the codes, ks and vs then being
+// the scales.
+struct AttnArgs {
+  const uint16_t *y;
+  long long ld;
+  int q_col, M, Hq, H, D;
+  const void *k, *v;
+  const uint8_t *ks, *vs;
+  int num_blocks, block_size;
+  const int32_t *block_table;
+  int B, max_blocks;
+  const int32_t *seq_len;
+  int rows_per_req, t0, window, sinks;
+  float scale_log2;  // scale * log2(e), times the K cache's unit
+  float v_unit;
+  uint16_t *out;
+  uint32_t *status;
+};
+cudaError_t launch_attention(const AttnArgs &a, bool q4, int num_sms, cudaStream_t s);
+
 }  // namespace mlora

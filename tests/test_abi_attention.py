@@ -1,0 +1,123 @@
+"""Host-side argument checks of the attention and 4-bit cache calls: every
+refusal returns before any CUDA call (this runs without a GPU)."""
+import ctypes
+
+import pytest
+import torch
+
+import speculative_lora_decoding_gb300 as ml
+from tests.test_abi import lib  # noqa: F401  (fixture: the built library)
+
+ARG, SHAPE, WS = 1, 2, 3
+P = ctypes.c_void_p(256)
+BIG = 1 << 40
+
+
+def _attention(lib, q4, **kw):  # noqa: F811
+    a = dict(y=P, M=4, ld=512, q_col=0, Hq=4, H=2, D=128, k=P, v=P, ks=P, vs=P, ku=1.0, vu=1.0, nb=8, bs=16, bt=P, B=2,
+             mb=4, seq=P, T=2, t0=0, window=0, sinks=0, scale=0.1, out=P, ws=P, wsb=BIG)
+    a.update(kw)
+    caches = [a["k"], a["ks"], a["v"], a["vs"], a["ku"], a["vu"]] if q4 else [a["k"], a["v"]]
+    fn = lib.mlora_attention_q4 if q4 else lib.mlora_attention
+    return fn(a["y"], a["M"], a["ld"], a["q_col"], a["Hq"], a["H"], a["D"], *caches, a["nb"], a["bs"], a["bt"], a["B"],
+              a["mb"], a["seq"], a["T"], a["t0"], a["window"], a["sinks"], a["scale"], a["out"], a["ws"], a["wsb"], None)
+
+
+SHAPES = [dict(M=5), dict(M=-1), dict(M=65537, B=65536), dict(ld=511), dict(q_col=-1), dict(q_col=1), dict(Hq=3),
+          dict(Hq=0), dict(H=0), dict(Hq=1), dict(D=0), dict(D=24), dict(D=272, ld=2000), dict(D=128, Hq=16384, ld=1 << 30),
+          dict(nb=0), dict(bs=0), dict(nb=1 << 20, bs=1 << 20), dict(B=0), dict(B=65537), dict(mb=0), dict(T=0),
+          dict(t0=-1), dict(window=-1), dict(sinks=-1)]
+ARGS = [dict(y=None), dict(out=None), dict(k=None), dict(v=None), dict(bt=None), dict(seq=None),
+        dict(out=ctypes.c_void_p(264)), dict(scale=float("nan")), dict(scale=float("inf"))]
+ARGS4 = [dict(ks=None), dict(vs=None), dict(k=ctypes.c_void_p(8)), dict(ks=ctypes.c_void_p(8)), dict(ku=0.0), dict(vu=-1.0),
+         dict(ku=float("nan")), dict(vu=float("inf")), dict(vu=3e38)]
+
+
+@pytest.mark.parametrize("q4", [False, True])
+def test_attention_refusals(lib, q4):  # noqa: F811
+    for kw in SHAPES:
+        assert _attention(lib, q4, **kw) == SHAPE, kw
+    for kw in ARGS + (ARGS4 if q4 else []):
+        assert _attention(lib, q4, **kw) == ARG, kw
+    for kw in (dict(ws=None), dict(wsb=16), dict(ws=ctypes.c_void_p(64))):
+        assert _attention(lib, q4, **kw) == WS, kw
+    # 2^30 token slots: fine over the bf16 cache, past 32 bits with two heads over the 4-bit one
+    over = _attention(lib, q4, nb=1 << 26, bs=16, ws=None)
+    assert over == (SHAPE if q4 else WS)
+
+
+def test_attention_workspace_bytes(lib):  # noqa: F811
+    f = lib.mlora_attention_workspace_bytes
+    assert f(640, 5, 40, 8, 128) > 0 and f(0, 1, 8, 8, 64) > 0
+    for bad in ((640, 5, 40, 7, 128), (640, 5, 40, 8, 100), (640, 0, 40, 8, 128), (-1, 1, 8, 8, 64), (65537, 1, 8, 8, 64),
+                (1, 1, 4, 8, 64), (1, 1, 8, 8, 320)):
+        assert f(*bad) == 0, bad
+
+
+def _write(lib, **kw):  # noqa: F811
+    a = dict(y=P, M=4, ld=96, k_col=32, v_col=64, H=2, D=16, bt=P, B=2, mb=4, seq=P, T=2, t0=0, kc=P, ks=P, vc=P, vs=P,
+             ku=1.0, vu=1.0, nb=8, bs=16, ws=P, wsb=BIG)
+    a.update(kw)
+    return lib.mlora_kv_write_q4(*(a[k] for k in ("y", "M", "ld", "k_col", "v_col", "H", "D", "bt", "B", "mb", "seq", "T",
+                                                  "t0", "kc", "ks", "vc", "vs", "ku", "vu", "nb", "bs", "ws", "wsb")), None)
+
+
+def _read(lib, **kw):  # noqa: F811
+    a = dict(kc=P, ks=P, vc=P, vs=P, ku=1.0, vu=1.0, H=2, D=16, bt=P, B=2, mb=4, start=P, end=P, rows=3, k=P, v=P, nb=8,
+             bs=16, ws=P, wsb=BIG)
+    a.update(kw)
+    return lib.mlora_kv_read_q4(*(a[k] for k in ("kc", "ks", "vc", "vs", "ku", "vu", "H", "D", "bt", "B", "mb", "start",
+                                                 "end", "rows", "k", "v", "nb", "bs", "ws", "wsb")), None)
+
+
+def test_kv_q4_refusals(lib):  # noqa: F811
+    odd = ctypes.c_void_p(264)
+    both = [dict(H=0), dict(D=8), dict(D=24), dict(H=1 << 17), dict(B=0), dict(B=65537), dict(mb=0), dict(nb=0), dict(bs=0),
+            dict(nb=1 << 27)]
+    for kw in both + [dict(M=5), dict(M=-1), dict(T=0), dict(t0=-1), dict(k_col=-1), dict(k_col=65), dict(v_col=65)]:
+        assert _write(lib, **kw) == SHAPE, kw
+    for kw in both + [dict(rows=-1), dict(rows=1 << 30)]:
+        assert _read(lib, **kw) == SHAPE, kw
+    null = [dict(kc=None), dict(ks=None), dict(vc=None), dict(vs=None), dict(bt=None), dict(kc=odd), dict(ks=odd),
+            dict(vc=odd), dict(vs=odd), dict(ku=0.0), dict(vu=float("nan")), dict(ku=1e38)]
+    for kw in null + [dict(y=None), dict(seq=None)]:
+        assert _write(lib, **kw) == ARG, kw
+    for kw in null + [dict(start=None), dict(end=None), dict(k=None), dict(v=None), dict(k=odd), dict(v=odd)]:
+        assert _read(lib, **kw) == ARG, kw
+    for kw in (dict(ws=None), dict(wsb=16), dict(ws=ctypes.c_void_p(64))):
+        assert _write(lib, **kw) == WS and _read(lib, **kw) == WS
+
+
+class _Ws:
+    ptr, nbytes = 256, BIG
+
+
+def test_binding_refusals():
+    """The binding checks shapes, dtypes, devices and contiguity before the library sees a pointer."""
+    z = lambda *s, t=torch.bfloat16: torch.zeros(s, dtype=t)  # noqa: E731
+    i32 = torch.int32
+    y, k, bt, seq = z(4, 512), z(8, 16, 2, 128), z(2, 4, t=i32), z(2, t=i32)
+    u8 = torch.uint8
+    four = [z(8, 2, 16, 64, t=u8), z(8, 2, 16, 8, t=u8), z(8, 2, 16, 64, t=u8), z(8, 2, 16, 8, t=u8)]
+    with pytest.raises(ValueError):
+        ml.attention(y, 0, 4, k, z(8, 16, 2, 64), bt, seq, 2, 0, ws=_Ws)
+    with pytest.raises(ValueError):
+        ml.attention(y, 0, 4, k, k, bt, z(3, t=i32), 2, 0, ws=_Ws, out=z(4, 512))
+    with pytest.raises(ValueError):
+        ml.attention(y, 0, 4, k, k, bt, seq, 2, 0, ws=_Ws, out=z(4, 256))
+    with pytest.raises(ValueError):                   # CPU tensors
+        ml.attention(y, 0, 4, k, k, bt, seq, 2, 0, ws=_Ws, out=z(4, 512))
+    with pytest.raises(TypeError):
+        ml.attention(y.float(), 0, 4, k, k, bt, seq, 2, 0, ws=_Ws, out=z(4, 512))
+    with pytest.raises(ValueError):
+        ml.attention_q4(y, 0, 4, four[0], four[1], four[2], z(8, 2, 16, 4, t=u8), bt, seq, 2, 0, ws=_Ws)
+    with pytest.raises(TypeError):
+        ml.attention_q4(y, 0, 4, four[0].to(torch.int8), *four[1:], bt, seq, 2, 0, ws=_Ws)
+    with pytest.raises(ValueError):
+        ml.kv_write_q4(y, 0, 256, 4, 128, bt, seq, 2, 0, *four, ws=_Ws)
+    with pytest.raises(ValueError):
+        ml.kv_read_q4(*four, bt, seq, z(3, t=i32), 4, ws=_Ws)
+    with pytest.raises(ValueError):
+        ml.kv_read_q4(*four, bt, seq, seq, -1, ws=_Ws)
+    with pytest.raises(ValueError):
+        ml.kv_read_q4(z(8, 2, 16, 60, t=u8), *four[1:], bt, seq, seq, 4, ws=_Ws)
