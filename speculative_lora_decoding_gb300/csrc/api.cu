@@ -675,9 +675,14 @@ static bool attn_heads_ok(int M, int rows_per_req, int Hq, int H, int D) {
          D % 16 == 0 && D <= 256 && (long long)Hq * D <= (1 << 20);
 }
 
+// Heads that the tensor-core kernels take.
+static bool attn_head_fast(int D) { return D == 64 || D == 128; }
+
 size_t mlora_attention_workspace_bytes(int M, int rows_per_req, int Hq, int H, int D) {
   if (!attn_heads_ok(M, rows_per_req, Hq, H, D)) return 0;
-  return WS_INIT_BYTES;
+  int sms = device_sms();
+  if (sms <= 0) sms = 160;
+  return align_up(WS_SCRATCH_OFF + (attn_head_fast(D) ? attn_rows_scratch_bytes(D, sms) : 0), 256);
 }
 
 static mlora_status attention_impl(const void *y, int M, int ld, int q_col, int Hq, int H, int D, const void *k,
@@ -690,7 +695,7 @@ static mlora_status attention_impl(const void *y, int M, int ld, int q_col, int 
       num_blocks < 1 || block_size < 1 || (long long)num_blocks * block_size > INT32_MAX / (q4 ? H : 1) || q_col < 0 ||
       (long long)q_col + (long long)Hq * D > ld)
     return MLORA_ERR_SHAPE;
-  if ((M > 0 && (!y || !out)) || !k || !v || !block_table || !seq_len || !isfinite(scale) || !aligned(out, 16))
+  if ((M > 0 && (!y || !out)) || !k || !v || !block_table || !seq_len || !std::isfinite(scale) || !aligned(out, 16))
     return MLORA_ERR_ARG;
   if (q4 && (!ks || !vs || !aligned4(k, ks, v, vs) || !unit_ok(k_unit) || !unit_ok(v_unit))) return MLORA_ERR_ARG;
   if (!workspace || !aligned(workspace, 256) || ws_bytes < mlora_attention_workspace_bytes(M, rows_per_req, Hq, H, D))
@@ -720,10 +725,17 @@ static mlora_status attention_impl(const void *y, int M, int ld, int q_col, int 
   a.window = window;
   a.sinks = sinks;
   a.scale_log2 = (float)((double)scale * k_unit * 1.4426950408889634);
+  if (!std::isfinite(a.scale_log2)) return MLORA_ERR_ARG;
   a.v_unit = v_unit;
   a.out = (uint16_t *)out;
   a.status = reinterpret_cast<uint32_t *>((uint8_t *)workspace + WS_STATUS_OFF);
-  return cuda_status(launch_attention(a, q4, sms, (cudaStream_t)stream));
+  if (M == 0) return MLORA_OK;
+  uint8_t *ws = (uint8_t *)workspace;
+  const bool fast = attn_head_fast(D) && ld % 8 == 0 && q_col % 8 == 0 && aligned(y, 16) && aligned(k, 16) && aligned(v, 16);
+  if (fast)
+    return cuda_status(launch_attn_rows(a, q4, reinterpret_cast<float *>(ws + WS_SCRATCH_OFF),
+                                        reinterpret_cast<uint32_t *>(ws + WS_COUNTERS_OFF), sms, (cudaStream_t)stream));
+  return cuda_status(launch_attn_general(a, q4, (cudaStream_t)stream));
 }
 
 mlora_status mlora_attention(const void *y, int M, int ld, int q_col, int Hq, int H, int D, const void *k_cache,

@@ -115,8 +115,7 @@ __global__ void __launch_bounds__(32 * AG_WARPS) attn_general_kernel(const AttnA
   }
 }
 
-cudaError_t launch_attention(const AttnArgs &a, bool q4, int num_sms, cudaStream_t s) {
-  if (a.M <= 0) return cudaSuccess;
+cudaError_t launch_attn_general(const AttnArgs &a, bool q4, cudaStream_t s) {
   const long long items = (long long)a.M * a.Hq;
   const unsigned grid = (unsigned)(items < (1 << 22) ? items : (1 << 22));
   if (q4) return launch_pdl(attn_general_kernel<true>, dim3(grid), dim3(32 * AG_WARPS), 0, s, a);

@@ -1,0 +1,1003 @@
+// Attention for few rows a request (draft steps, verify passes): heads of 64
+// and 128 on the tensor cores, over the bf16 or the 4-bit paged cache.
+//
+// With R = rows x (query heads per cache head) query rows against each cache
+// head, every cached value takes part in R multiply-adds per byte or two: the
+// kernel streams the cache once and is bound by HBM, so it is built around the
+// loads.
+//
+// Work.  A unit is (request, cache head, up to 32 query rows).  The tiles (16
+// or 32 positions) of all units, in order, are cut into equal contiguous
+// shares, one per warp (8 warps to a CTA, one CTA per SM), so mixed lengths
+// balance by themselves; every CTA finds its shares from the lengths on the
+// device.  A cut that would leave less than AR_SNAP tiles of a unit on one side
+// moves to the unit's end.  A warp has its own ring of asynchronous copies,
+// query rows, running maximum, sums and output accumulators, and there is no
+// barrier until all tiles are done: a unit within a warp's share is written
+// from registers.  What is left at the end are the units that cuts went
+// through: their parts are joined in order, first within the CTA, then, for
+// the units that several CTAs share, by the last of these to arrive.
+//
+// Products.  The cache is the M side of m16n8k16 MMAs and the query rows the N
+// side, so 5 or 25 rows pad to 8 or 32 and not to 16 or 128:
+//   S^T[positions, rows] = K Q^T,   O^T[D, rows] += V^T P^T.
+// P^T moves from S^T's accumulator layout to the second product's operand by
+// 8x8 register transposes.
+//
+// The running maximum moves only when some score exceeds it by 8 (in log2
+// units): weights then stay below 2^8, which fp32 sums and fp16/bf16 weights
+// hold, and most tiles need no exchange between lanes.
+//
+// 4-bit cache: codes go from shared memory to fp16 operands in registers by
+// cvt and one multiply by their scale, exactly.  The order of the head's D in
+// the first product and of the positions in the second is free as long as
+// both operands agree, and is chosen so that a lane's 16 bytes of K codes and
+// 8 bytes of V codes are contiguous.
+#include "common.cuh"
+#include "e2m1.cuh"
+#include "launch.h"
+#include "prob.cuh"
+
+namespace mlora {
+
+constexpr int AR_WARPS = 8;
+constexpr int AR_THREADS = 32 * AR_WARPS;
+constexpr float AR_EMPTY = -3.402823466e38f;  // the maximum of nothing: any score replaces it
+constexpr float AR_SLACK = 8.f;               // log2 units a score may exceed the running maximum by
+
+constexpr int AR_SNAP = 3;                    // tiles
+constexpr int AR_MIN_TILES = 2;               // tiles a warp gets at least, on average
+
+template <bool Q4, int D, int NR>
+struct ArCfg {
+  static constexpr int TILE = Q4 && NR < 4 ? 32 : 16;  // positions a warp takes at a time (16: registers)
+  static constexpr int MT = TILE / 16;
+  static constexpr int STAGES = Q4 ? 128 / TILE : 2;
+  static constexpr int KROW = Q4 ? D / 2 : D * 2;  // bytes of a position's row
+  static constexpr int SROW = Q4 ? D / 16 : 0;     // bytes of its scales
+  static constexpr int V_OFF = TILE * KROW;
+  static constexpr int KS_OFF = 2 * TILE * KROW;
+  static constexpr int VS_OFF = KS_OFF + TILE * SROW;
+  static constexpr int STAGE_BYTES = VS_OFF + TILE * SROW;
+  static constexpr int ROWS = 8 * NR;
+  static constexpr int FRAG = D / 16 * NR * 32;    // float4 of a warp's accumulators
+  static constexpr int RING = STAGES * STAGE_BYTES;
+  static_assert(RING >= FRAG * 16, "a warp's accumulators go where its ring was");
+  static constexpr int QBYTES = ROWS * D * 2;
+  static constexpr int Q_OFF = AR_WARPS * RING;
+  static constexpr int QMUL_OFF = Q_OFF + AR_WARPS * QBYTES;
+  static constexpr int M_OFF = QMUL_OFF + AR_WARPS * ROWS * 4;      // [2 AR_WARPS][ROWS]
+  static constexpr int L_OFF = M_OFF + 2 * AR_WARPS * ROWS * 4;
+  static constexpr int MASK_OFF = L_OFF + 2 * AR_WARPS * ROWS * 4;  // [AR_WARPS][STAGES]
+  static constexpr int MISC_OFF = MASK_OFF + AR_WARPS * STAGES * 4;
+  static constexpr int SMEM = MISC_OFF + 1024;
+};
+
+// A part of a unit that a warp computed: the warp's last tiles (their sums in
+// its ring's memory) or its first (their sums in global memory).
+struct ArPiece {
+  long long g0;  // the unit's first tile, counted over all units; -1: no piece
+  int b, h, rt, nt;
+};
+struct ArShared {
+  long long bound[AR_WARPS + 1];            // the warps' cuts, counted over all units
+  int at_b[AR_WARPS + 1], at_u[AR_WARPS + 1], at_tile[AR_WARPS + 1];
+  long long sums[AR_WARPS];
+  ArPiece piece[2 * AR_WARPS];              // in order: warp 0's first tiles, warp 0's last, ...
+  int last;
+};
+static_assert(sizeof(ArShared) <= 1024, "ArShared");
+
+// The positions that some row of a request sees: sinks [0, sink) and
+// [w0, n), w0 rounded down to a tile; tiles of the sinks come first.
+struct ArRange {
+  int w0, n, sink, st, nt;
+};
+
+// A place in the flattened list of tiles.
+struct ArCursor {
+  int i;  // tiles past the warp's first
+  int b, h, rt, tile;
+  ArRange r;
+};
+
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void *src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_small(uint32_t dst, const void *src, bool there) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(there ? N : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void ldsm_x4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm_x4_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+
+template <bool F16>
+__device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                          uint2 b) {
+  if (F16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b.x), "r"(b.y));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b.x), "r"(b.y));
+}
+
+template <bool F16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  uint32_t r;
+  if (F16)
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint4 lds_v4(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint2 lds_v2(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t lds_u32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t lds_u16(uint32_t a) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t lds_u8(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+
+// 4-bit tiles, positions of a 16-position group: the row of S^T (and of the K
+// rows in shared memory) that holds position t, and back.
+__device__ __forceinline__ int q4_row_of(int t) { return 2 * (t & 3) + ((t >> 2) & 1) + (t & 8); }
+__device__ __forceinline__ int q4_pos_of(int i) { return (i & 8) + ((i & 7) >> 1) + 4 * (i & 1); }
+
+// Byte offset of 8 bytes of V codes (D = 128: elements 16 g ..; rows of 64
+// bytes whose 16-byte pieces trade places so that four rows' pieces fall on
+// different banks).
+__device__ __forceinline__ int q4_v_off128(int t, int g) {
+  return t * 64 + (((g >> 1) ^ (((t >> 1) & 1) << 1)) * 16) + (g & 1) * 8;
+}
+
+struct ArArgs {
+  AttnArgs a;
+  int G, n_rt, RT;   // query heads per cache head; row tiles per (request, head), rows in each
+  int extent;        // positions that a block table reaches
+  int bs_shift;      // log2 of the page size, or -1
+  float *part;       // sums of units in parts: a slot per warp, then two per CTA (AR_SLOT floats each:
+                     // 32 (maximum, sum) pairs, then the accumulators in fragment order)
+  uint32_t *counters;
+};
+
+template <int D>
+constexpr size_t AR_SLOT = 64 + 32 * D;
+
+template <bool Q4, int D, int NR>
+__global__ void __launch_bounds__(AR_THREADS, 1) attn_rows_kernel(const ArArgs p) {
+  using C = ArCfg<Q4, D, NR>;
+  constexpr int TILE = C::TILE, MT = C::MT, S = C::STAGES, KS = D / 16, MI = D / 16, GD = D / 8;
+  extern __shared__ __align__(128) uint8_t smem[];
+  const AttnArgs &a = p.a;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+  const int cta = blockIdx.x, T = a.rows_per_req, U = a.H * p.n_rt;
+  float *qmul = reinterpret_cast<float *>(smem + C::QMUL_OFF) + warp * C::ROWS;
+  float *sm_m = reinterpret_cast<float *>(smem + C::M_OFF);
+  float *sm_l = reinterpret_cast<float *>(smem + C::L_OFF);
+  uint32_t *vmask = reinterpret_cast<uint32_t *>(smem + C::MASK_OFF);
+  ArShared &sh = *reinterpret_cast<ArShared *>(smem + C::MISC_OFF);
+  const uint32_t ring = smem_addr(smem) + warp * C::RING;
+  uint8_t *qsmem = smem + C::Q_OFF + warp * C::QBYTES;
+  const uint32_t qf = smem_addr(qsmem) + lane * 8;
+
+  grid_launch_dependents();
+  grid_dependency_wait();  // y, the cache and the lengths come from the kernels just before
+
+  auto rows_of = [&](int b) { return min(T, a.M - b * T); };  // rows of request b in this pass
+  auto range_of = [&](int b) {
+    ArRange r = {0, 0, 0, 0, 0};
+    const int tb = rows_of(b);
+    const int L = b < a.B && tb > 0 ? __ldg(a.seq_len + b) : -1;
+    if (L < 0) return r;
+    const long long p0 = (long long)L + a.t0, last = p0 + tb - 1;
+    r.n = (int)min(last + 1, (long long)p.extent);
+    if (a.window && p0 >= a.window) {
+      r.w0 = (int)min(p0 - a.window + 1, (long long)r.n) & ~(TILE - 1);
+      r.sink = min(a.sinks, r.w0);
+      r.st = (r.sink + TILE - 1) / TILE;
+    }
+    r.nt = r.st + (r.n - r.w0 + TILE - 1) / TILE;
+    return r;
+  };
+
+  // Requests that see nothing: zeros.  Rows past the table's reach: status.
+  for (int b = cta; b < a.B; b += gridDim.x) {
+    const int tb = rows_of(b);
+    if (tb <= 0) break;
+    const ArRange r = range_of(b);
+    if (r.nt == 0) {
+      uint4 *dst = reinterpret_cast<uint4 *>(a.out + (size_t)b * T * a.Hq * D);
+      const size_t n = (size_t)tb * a.Hq * D / 8;
+      for (size_t i = tid; i < n; i += AR_THREADS) dst[i] = make_uint4(0, 0, 0, 0);
+    }
+    if (tid == 0) {
+      const int L = __ldg(a.seq_len + b);
+      if (L >= 0 && (long long)L + a.t0 + tb > p.extent) raise_status(a.status, MLORA_DEV_BAD_SLOT);
+    }
+  }
+
+  // All tiles, the CTAs among which they are cut, and this CTA's cuts.
+  long long total = 0;
+  for (int base = 0; base < a.B; base += AR_THREADS) {
+    long long v = base + tid < a.B ? range_of(base + tid).nt : 0;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    total += v;
+  }
+  if (lane == 0) sh.sums[warp] = total;
+  if (tid < 2 * AR_WARPS) sh.piece[tid].g0 = -1;
+  __syncthreads();
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < AR_WARPS; ++w) total += sh.sums[w];
+  total *= U;
+  if (total == 0) return;
+  // A CTA's share is at least 16 tiles (or all there are): wider than two
+  // moved cuts, so that no CTA is left without tiles.
+  const long long want = max(total / (AR_WARPS * AR_MIN_TILES), 1ll);
+  const int P = (int)min((long long)gridDim.x, want);
+  const int NW = P * AR_WARPS;
+  if (cta >= P) return;
+  // Where the cut at `o` of a unit's nt tiles goes.
+  auto snap = [](int o, int nt) {
+    if (o < AR_SNAP || nt - o < AR_SNAP) return 2 * o < nt ? 0 : nt;
+    return o;
+  };
+  __syncthreads();  // sums are written again
+  {
+    long long before = 0;
+    for (int base = 0; base < a.B; base += AR_THREADS) {
+      const int nt = base + tid < a.B ? range_of(base + tid).nt : 0;
+      long long v = nt;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long u = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += u;
+      }
+      if (lane == 31) sh.sums[warp] = v;
+      __syncthreads();
+      long long off = before, all = 0;
+#pragma unroll
+      for (int w = 0; w < AR_WARPS; ++w) {
+        if (w < warp) off += sh.sums[w];
+        all += sh.sums[w];
+      }
+      const long long lo = (off + v - nt) * U, hi = (off + v) * U;
+      for (int w = 0; w <= AR_WARPS; ++w) {
+        const long long raw = total * (cta * AR_WARPS + w) / NW;
+        if (lo <= raw && raw < hi) {
+          const int u = (int)((raw - lo) / nt);
+          const int o = snap((int)(raw - lo - (long long)u * nt), nt);
+          sh.at_b[w] = base + tid;
+          sh.at_u[w] = u;
+          sh.at_tile[w] = o;
+          sh.bound[w] = lo + (long long)u * nt + o;
+        } else if (raw == total && hi == total && nt > 0) {
+          sh.bound[w] = total;
+        }
+      }
+      before += all;
+      __syncthreads();
+    }
+  }
+  const long long s0 = sh.bound[warp];
+  const int count = (int)(sh.bound[warp + 1] - s0);
+
+  auto advance = [&](ArCursor &x, int k) {
+    x.i += k;
+    x.tile += k;
+    while (x.i < count && x.tile >= x.r.nt) {
+      x.tile -= x.r.nt;
+      if (++x.rt < p.n_rt) continue;
+      x.rt = 0;
+      if (++x.h < a.H) continue;
+      x.h = 0;
+      do {
+        ++x.b;
+        x.r = range_of(x.b);
+      } while (x.r.nt == 0 && x.b < a.B);
+      if (x.b >= a.B) x.i = count;  // (not reached: the share ends within the tiles)
+    }
+  };
+  auto tile_start = [&](const ArRange &r, int tile) {
+    return tile < r.st ? tile * TILE : r.w0 + (tile - r.st) * TILE;
+  };
+
+  ArCursor seg = {0, 0, 0, 0, 0, {0, 0, 0, 0, 0}};  // the segment (a unit's tiles within the share) being computed
+  if (count > 0) {
+    seg.b = sh.at_b[warp];
+    seg.r = range_of(seg.b);
+    seg.h = sh.at_u[warp] / p.n_rt;
+    seg.rt = sh.at_u[warp] - seg.h * p.n_rt;
+    seg.tile = sh.at_tile[warp];
+    advance(seg, 0);  // a cut that moved to a unit's end starts at the next unit
+  }
+
+  // --- loads ---------------------------------------------------------------
+  ArCursor nx = seg;  // the next tile this warp will ask for
+  int n_blk = -1, n_off = 0;
+  bool n_in = false;
+  // The page of each of the next tile's positions, asked for ahead of the copies.
+  auto look_up = [&]() {
+    n_in = false;
+    n_blk = -1;
+    if (nx.i < count) {
+      const int j = tile_start(nx.r, nx.tile) + (lane & (TILE - 1));
+      n_in = j < (nx.tile < nx.r.st ? nx.r.sink : nx.r.n);
+      if (n_in) {
+        const int page = p.bs_shift >= 0 ? j >> p.bs_shift : j / a.block_size;
+        n_off = j - page * a.block_size;
+        n_blk = __ldg(a.block_table + (size_t)nx.b * a.max_blocks + page);
+      }
+    }
+  };
+  auto issue = [&](int stage) {
+    if (nx.i < count) {
+      int slot = -1;
+      if (n_in) {
+        if (n_blk >= 0 && n_blk < a.num_blocks)
+          slot = Q4 ? (n_blk * a.H + nx.h) * a.block_size + n_off : n_blk * a.block_size + n_off;
+        else
+          raise_status(a.status, MLORA_DEV_BAD_SLOT);
+      }
+      const uint32_t there = __ballot_sync(0xffffffffu, slot >= 0);
+      if (lane == 0) vmask[warp * S + stage] = there;
+      const uint32_t dst = ring + stage * C::STAGE_BYTES;
+      constexpr int CH = C::KROW / 16;           // 16-byte pieces of a row
+      constexpr int PER = 32 / CH;               // rows per instruction
+      const int ch = lane & (CH - 1);
+#pragma unroll
+      for (int i = 0; i < TILE / PER; ++i) {
+        const int t = i * PER + lane / CH;
+        const int s = __shfl_sync(0xffffffffu, slot, t);
+        const size_t row = Q4 ? (size_t)max(s, 0) : (size_t)max(s, 0) * a.H + nx.h;
+        const size_t off = row * C::KROW + ch * 16;
+        uint32_t ko, vo;
+        if (Q4) {
+          ko = ((t & 16) + q4_row_of(t & 15)) * C::KROW + ch * 16;
+          vo = D == 128 ? t * C::KROW + (ch ^ (((t >> 1) & 1) << 1)) * 16 : t * C::KROW + ch * 16;
+        } else {
+          ko = vo = t * C::KROW + (ch ^ (t & 7)) * 16;
+        }
+        cp_async_16(dst + ko, static_cast<const uint8_t *>(a.k) + off, s >= 0);
+        cp_async_16(dst + C::V_OFF + vo, static_cast<const uint8_t *>(a.v) + off, s >= 0);
+      }
+      if (Q4 && lane < TILE) {
+        const size_t off = (size_t)max(slot, 0) * C::SROW;
+        cp_async_small<Q4 ? C::SROW : 4>(dst + C::KS_OFF + ((lane & 16) + q4_row_of(lane & 15)) * C::SROW, a.ks + off,
+                                         slot >= 0);
+        cp_async_small<Q4 ? C::SROW : 4>(dst + C::VS_OFF + lane * C::SROW, a.vs + off, slot >= 0);
+      }
+      advance(nx, 1);
+      look_up();
+    }
+    cp_async_commit();
+  };
+
+  // --- query rows: the warp's own, as the operand's fragments --------------
+  auto load_q = [&](const ArCursor &x, int n_rows) {
+    uint2 qv[C::ROWS];  // a lane holds elements 4 lane .. + 3 of every row
+#pragma unroll
+    for (int lr = 0; lr < C::ROWS; ++lr) {
+      qv[lr] = make_uint2(0, 0);
+      if (lr < n_rows && 4 * lane < D) {
+        const int r = x.rt * p.RT + lr, t = r / p.G;
+        const uint16_t *src = a.y + (size_t)(x.b * T + t) * a.ld + a.q_col + (size_t)(x.h * p.G + r - t * p.G) * D;
+        qv[lr] = *reinterpret_cast<const uint2 *>(src + 4 * lane);
+      }
+    }
+    __syncwarp();  // the rows before these have been read by every lane
+#pragma unroll
+    for (int lr = 0; lr < C::ROWS; ++lr) {
+      const int n = lr >> 3, row = lr & 7;
+      if (Q4) {
+        // fp16 relative to the row's largest magnitude (a power of two, given
+        // back to the scores): exact but for entries 2^-14 below it.
+        uint32_t mx = max(max(qv[lr].x & 0x7FFFu, (qv[lr].x >> 16) & 0x7FFFu),
+                          max(qv[lr].y & 0x7FFFu, (qv[lr].y >> 16) & 0x7FFFu));
+        mx = __reduce_max_sync(0xffffffffu, mx);
+        const uint32_t e = min(max(mx >> 7, 1u), 253u);
+        const float down = __uint_as_float((254u - e) << 23);
+        if (lane == 0) qmul[lr] = __uint_as_float(e << 23) * a.scale_log2;
+        if (4 * lane < D) {
+          uint2 f;
+          f.x = pack2<true>(__uint_as_float(qv[lr].x << 16) * down, __uint_as_float(qv[lr].x & 0xFFFF0000u) * down);
+          f.y = pack2<true>(__uint_as_float(qv[lr].y << 16) * down, __uint_as_float(qv[lr].y & 0xFFFF0000u) * down);
+          const int cc = lane / KS, ks = lane % KS;  // elements 4 KS cc + 4 ks ..
+          *reinterpret_cast<uint2 *>(qsmem + ((ks * NR + n) * 32 + row * 4 + cc) * 8) = f;
+        }
+      } else if (4 * lane < D) {
+        const int ks = lane >> 2, q = lane & 3, c0 = 2 * (q & 1);
+        uint8_t *f = qsmem + ((ks * NR + n) * 32 + row * 4 + c0) * 8 + (q >> 1) * 4;
+        *reinterpret_cast<uint32_t *>(f) = qv[lr].x;
+        *reinterpret_cast<uint32_t *>(f + 8) = qv[lr].y;
+      }
+    }
+    __syncwarp();
+  };
+
+  // --- outputs --------------------------------------------------------------
+  auto row_ptr = [&](int b, int h, int rt, int lr) {
+    const int r = rt * p.RT + lr, t = r / p.G;
+    return a.out + ((size_t)(b * T + t) * a.Hq + h * p.G + r - t * p.G) * D;
+  };
+  // 16 elements of D (accumulator group mi) of rows 8n .. 8n + 7 from the lanes' fragments.
+  auto write_frag = [&](const float (&v)[4], int mi, int n, int b, int h, int rt, int n_rows) {
+    if (Q4) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int lr = 8 * n + 2 * c + e;
+        if (lr < n_rows)
+          *reinterpret_cast<uint32_t *>(row_ptr(b, h, rt, lr) + GD * g + 2 * mi) = pack2<false>(v[e], v[2 + e]);
+      }
+    } else {
+      const uint32_t x0 = transpose_8x8(pack2<false>(v[0], v[1])), x1 = transpose_8x8(pack2<false>(v[2], v[3]));
+      const int lr = 8 * n + g;
+      if (lr < n_rows) {
+        uint32_t *dst = reinterpret_cast<uint32_t *>(row_ptr(b, h, rt, lr) + 16 * mi + 2 * c);
+        dst[0] = x0;
+        dst[4] = x1;
+      }
+    }
+  };
+  auto weight = [&](float l) { return l != 0.f ? a.v_unit / l : 0.f; };
+  // A row that saw nothing is zeros, whatever multiplied its weights of 0.
+  auto scaled = [](float v, float w) { return w != 0.f ? v * w : 0.f; };
+
+  look_up();
+#pragma unroll
+  for (int s = 0; s < S; ++s) issue(s);
+
+  int stage = 0;
+  while (seg.i < count) {
+    // --- a segment: tiles [seg.tile, end) of one unit ----------------------
+    const int ta = seg.tile, end = min(seg.r.nt, ta + count - seg.i);
+    const long long p0 = (long long)__ldg(a.seq_len + seg.b) + a.t0;
+    const int n_rows = min(p.RT, rows_of(seg.b) * p.G - seg.rt * p.RT);
+    const long long plast = p0 + rows_of(seg.b) - 1;
+    load_q(seg, n_rows);
+    // The rows' steps within the pass, as bytes past the first row's.
+    const int step0 = seg.rt * p.RT / p.G;
+    uint32_t steps[(2 * NR + 3) / 4];
+#pragma unroll
+    for (int i = 0; i < 2 * NR; ++i) {
+      const uint32_t d = (uint32_t)((seg.rt * p.RT + 8 * (i >> 1) + 2 * c + (i & 1)) / p.G - step0) << (8 * (i & 3));
+      steps[i >> 2] = (i & 3) ? steps[i >> 2] | d : d;
+    }
+    auto step_of = [&](int n, int e) { return step0 + (int)((steps[(2 * n + e) >> 2] >> (8 * ((2 * n + e) & 3))) & 0xFFu); };
+    float o[MI][NR][4], m[NR][2], l[NR][2], mul[NR][2];
+#pragma unroll
+    for (int n = 0; n < NR; ++n) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        m[n][e] = AR_EMPTY;
+        l[n][e] = 0.f;
+        mul[n][e] = Q4 ? qmul[8 * n + 2 * c + e] : a.scale_log2;
+      }
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[i][n][k] = 0.f;
+    }
+
+    for (int tile = ta; tile < end; ++tile) {
+      cp_async_wait<S - 1>();
+      __syncwarp();
+      const uint32_t st = ring + stage * C::STAGE_BYTES;
+      const uint32_t there = vmask[warp * S + stage];
+      const int j0 = tile_start(seg.r, tile);
+
+      // S^T = K Q^T
+      float s[MT][NR][4];
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int n = 0; n < NR; ++n)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) s[t][n][k] = 0.f;
+      if (Q4) {
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+          uint32_t w[2][4], sc[2][2];
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const int row = 16 * t + 8 * half + g;
+            if (D == 128) {
+              const uint4 v = lds_v4(st + row * C::KROW + c * 16);
+              w[half][0] = v.x; w[half][1] = v.y; w[half][2] = v.z; w[half][3] = v.w;
+              const uint32_t two = e4m3x2_to_f16(lds_u16(st + C::KS_OFF + row * C::SROW + 2 * c));
+              sc[half][0] = __byte_perm(two, two, 0x1010);
+              sc[half][1] = __byte_perm(two, two, 0x3232);
+            } else {
+              const uint2 v = lds_v2(st + row * C::KROW + c * 8);
+              w[half][0] = v.x; w[half][1] = v.y;
+              const uint32_t one = e4m3x2_to_f16(lds_u8(st + C::KS_OFF + row * C::SROW + c));
+              sc[half][0] = __byte_perm(one, one, 0x1010);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i) {
+            uint32_t lo[4], hi[4];
+            e2m1x8_to_f16(w[0][i], lo);
+            e2m1x8_to_f16(w[1][i], hi);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              lo[k] = hmul2(lo[k], sc[0][i >> 1]);
+              hi[k] = hmul2(hi[k], sc[1][i >> 1]);
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+              for (int n = 0; n < NR; ++n)
+                mma_16816<true>(s[t][n], lo[2 * k], hi[2 * k], lo[2 * k + 1], hi[2 * k + 1],
+                                lds_v2(qf + ((2 * i + k) * NR + n) * 256));
+          }
+        }
+      } else {
+        const int row = (lane & 7) + ((lane >> 3) & 1) * 8;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          uint32_t k4[4];
+          ldsm_x4(k4, st + row * C::KROW + (((2 * ks + (lane >> 4)) ^ (row & 7)) * 16));
+#pragma unroll
+          for (int n = 0; n < NR; ++n)
+            mma_16816<false>(s[0][n], k4[0], k4[1], k4[2], k4[3], lds_v2(qf + (ks * NR + n) * 256));
+        }
+      }
+
+      // Scores; hidden ones become -infinity.
+      const int jl = j0 + TILE - 1;
+      const bool edge = there != 0xffffffffu || jl > p0 ||
+                        (a.window && !(j0 > plast - a.window || jl < a.sinks));
+      auto sees = [&](int lr, int step, int jj) {  // row lr (at `step` of the pass), position j0 + jj
+        if (lr >= n_rows || !((there >> jj) & 1u)) return false;
+        const long long pr = p0 + step, j = j0 + jj;
+        return j <= pr && (!a.window || j > pr - a.window || j < a.sinks);
+      };
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int n = 0; n < NR; ++n)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) s[t][n][k] *= mul[n][k & 1];
+      if (edge) {
+#pragma unroll
+        for (int n = 0; n < NR; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int lr = 8 * n + 2 * c + e;
+#pragma unroll
+            for (int t = 0; t < MT; ++t)
+#pragma unroll
+              for (int half = 0; half < 2; ++half) {
+                const int i = 8 * half + g, jj = 16 * t + (Q4 ? q4_pos_of(i) : i);
+                if (!sees(lr, step_of(n, e), jj)) s[t][n][2 * half + e] = -__builtin_huge_valf();
+              }
+          }
+      }
+
+      // Move the maximum when some score lies far above it.
+      bool far = false;
+      float mx[NR][2];
+#pragma unroll
+      for (int n = 0; n < NR; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          mx[n][e] = fmaxf(s[0][n][e], s[0][n][2 + e]);
+          if (MT == 2) mx[n][e] = fmaxf(mx[n][e], fmaxf(s[MT - 1][n][e], s[MT - 1][n][2 + e]));
+          far |= mx[n][e] > m[n][e] + AR_SLACK;
+        }
+      if (__any_sync(0xffffffffu, far)) {
+#pragma unroll
+        for (int n = 0; n < NR; ++n) {
+          float corr[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float v = mx[n][e];
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, x));
+            const float mn = fmaxf(m[n][e], v);
+            corr[e] = exp2_hw(m[n][e] - mn);
+            m[n][e] = mn;
+            l[n][e] *= corr[e];
+          }
+#pragma unroll
+          for (int i = 0; i < MI; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) o[i][n][k] *= corr[k & 1];
+        }
+      }
+      // Weights, and their transposes as the second product's operand.
+      uint2 pb[MT][NR];
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int n = 0; n < NR; ++n) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            s[t][n][k] = exp2_hw(s[t][n][k] - m[n][k & 1]);
+            l[n][k & 1] += s[t][n][k];
+          }
+          pb[t][n].x = transpose_8x8(pack2<Q4>(s[t][n][0], s[t][n][1]));
+          pb[t][n].y = transpose_8x8(pack2<Q4>(s[t][n][2], s[t][n][3]));
+        }
+
+      // 0 times an infinity or a NaN that a row does not see would reach it
+      // through the product: such tiles (rows that see different positions,
+      // with values that are not finite) are added up one position at a time.
+      bool odd = false;
+      if (edge) {
+        if (Q4) {
+          for (int i = lane; i < TILE * C::SROW; i += 32) odd |= (lds_u8(st + C::VS_OFF + i) & 0x7Fu) == 0x7Fu;
+        } else {
+          for (int i = lane; i < TILE * C::KROW / 16; i += 32) {
+            const uint4 v = lds_v4(st + C::V_OFF + i * 16);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              odd |= (w[k] & 0x7F80u) == 0x7F80u || (w[k] & 0x7F800000u) == 0x7F800000u;
+          }
+        }
+        odd = __any_sync(0xffffffffu, odd);
+      }
+      if (odd) {
+        for (int i = 0; i < TILE; ++i) {
+          const int i16 = i & 15, jj = (i & 16) + (Q4 ? q4_pos_of(i16) : i16);
+          const int src = (i16 & 7) * 4 + c;
+#pragma unroll
+          for (int n = 0; n < NR; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float w = 0.f;
+#pragma unroll
+              for (int t = 0; t < MT; ++t)
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                  const float x = __shfl_sync(0xffffffffu, s[t][n][2 * half + e], src);
+                  if (t == i >> 4 && half == (i16 >> 3)) w = x;
+                }
+              const bool vis = sees(8 * n + 2 * c + e, step_of(n, e), jj);
+#pragma unroll
+              for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                  float v;
+                  if (Q4) {
+                    const int gd = D / 8, d = gd * g + 2 * mi + half;
+                    const uint32_t at =
+                        D == 128 ? q4_v_off128(jj, g) + mi : jj * C::KROW + g * 4 + mi;
+                    uint32_t f[4];
+                    const uint32_t byte = lds_u8(st + C::V_OFF + at);
+                    e2m1x8_to_f16(half ? byte >> 4 : byte & 15u, f);
+                    v = f16_lo(f[0]) * e4m3_to_float(lds_u8(st + C::VS_OFF + jj * C::SROW + d / 16));
+                  } else {
+                    const int d = 16 * mi + 8 * half + g;
+                    v = bf16_bits_to_float((uint16_t)lds_u16(st + C::V_OFF + jj * C::KROW +
+                                                             (((d >> 3) ^ (jj & 7)) * 16) + (d & 7) * 2));
+                  }
+                  if (vis) o[mi][n][2 * half + e] += w * v;
+                }
+            }
+        }
+      } else if (Q4) {
+        // O^T += V^T P^T; a lane's D/8 elements of four positions.
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+          uint32_t w[4][2], sv[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int row = 16 * t + c + 4 * e;
+            if (D == 128) {
+              const uint2 v = lds_v2(st + C::V_OFF + q4_v_off128(row, g));
+              w[e][0] = v.x;
+              w[e][1] = v.y;
+              sv[e] = lds_u8(st + C::VS_OFF + row * C::SROW + g);
+            } else {
+              w[e][0] = lds_u32(st + C::V_OFF + row * C::KROW + g * 4);
+              sv[e] = lds_u8(st + C::VS_OFF + row * C::SROW + (g >> 1));
+            }
+          }
+          const uint32_t s01 = e4m3x2_to_f16(sv[0] | (sv[1] << 8)), s23 = e4m3x2_to_f16(sv[2] | (sv[3] << 8));
+#pragma unroll
+          for (int i = 0; i < D / 64; ++i) {
+            uint32_t x01[4], y01[4], x23[4], y23[4];
+            constexpr uint32_t LO = 0x0F0F0F0Fu;
+            e2m1x8_to_f16((w[0][i] & LO) | ((w[1][i] << 4) & ~LO), x01);
+            e2m1x8_to_f16(((w[0][i] >> 4) & LO) | (w[1][i] & ~LO), y01);
+            e2m1x8_to_f16((w[2][i] & LO) | ((w[3][i] << 4) & ~LO), x23);
+            e2m1x8_to_f16(((w[2][i] >> 4) & LO) | (w[3][i] & ~LO), y23);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t a0 = hmul2(x01[k], s01), a1 = hmul2(y01[k], s01);
+              const uint32_t a2 = hmul2(x23[k], s23), a3 = hmul2(y23[k], s23);
+#pragma unroll
+              for (int n = 0; n < NR; ++n) mma_16816<true>(o[4 * i + k][n], a0, a1, a2, a3, pb[t][n]);
+            }
+          }
+        }
+      } else {
+        const int row = (lane & 7) + (lane >> 4) * 8;
+#pragma unroll
+        for (int mi = 0; mi < MI; ++mi) {
+          uint32_t v4[4];
+          ldsm_x4_trans(v4, st + C::V_OFF + row * C::KROW + (((2 * mi + ((lane >> 3) & 1)) ^ (row & 7)) * 16));
+#pragma unroll
+          for (int n = 0; n < NR; ++n) mma_16816<false>(o[mi][n], v4[0], v4[1], v4[2], v4[3], pb[0][n]);
+        }
+      }
+
+      __syncwarp();  // the stage has been read by every lane
+      issue(stage);
+      stage = stage + 1 == S ? 0 : stage + 1;
+    }
+
+#pragma unroll
+    for (int n = 0; n < NR; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], x);
+    if (ta == 0 && end == seg.r.nt) {  // the whole unit: written
+#pragma unroll
+      for (int n = 0; n < NR; ++n) {
+        const float w[2] = {weight(l[n][0]), weight(l[n][1])};
+        if (Q4) {
+          // A lane's elements of a row are D/8 in a run.
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int lr = 8 * n + 2 * c + e;
+            uint32_t v[MI];
+#pragma unroll
+            for (int mi = 0; mi < MI; ++mi)
+              v[mi] = pack2<false>(scaled(o[mi][n][e], w[e]), scaled(o[mi][n][2 + e], w[e]));
+            if (lr < n_rows) {
+              uint4 *dst = reinterpret_cast<uint4 *>(row_ptr(seg.b, seg.h, seg.rt, lr) + GD * g);
+#pragma unroll
+              for (int k = 0; k < MI / 4; ++k) dst[k] = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int mi = 0; mi < MI; ++mi) {
+            const float v[4] = {scaled(o[mi][n][0], w[0]), scaled(o[mi][n][1], w[1]), scaled(o[mi][n][2], w[0]),
+                                scaled(o[mi][n][3], w[1])};
+            write_frag(v, mi, n, seg.b, seg.h, seg.rt, n_rows);
+          }
+        }
+      }
+    } else {  // a part of it: kept, in shared memory if it is the warp's last
+      const bool last = seg.i + end - ta == count;
+      const int pc = 2 * warp + last;
+      if (last) cp_async_wait<0>();  // (the groups left are empty; the ring's memory is free)
+      __syncwarp();
+      float4 *dst = last ? reinterpret_cast<float4 *>(smem + warp * C::RING)
+                         : reinterpret_cast<float4 *>(p.part + (size_t)(cta * AR_WARPS + warp) * AR_SLOT<D> + 64);
+#pragma unroll
+      for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+        for (int n = 0; n < NR; ++n)
+          dst[(mi * NR + n) * 32 + lane] = make_float4(o[mi][n][0], o[mi][n][1], o[mi][n][2], o[mi][n][3]);
+      if (g == 0) {
+#pragma unroll
+        for (int n = 0; n < NR; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            sm_m[pc * C::ROWS + 8 * n + 2 * c + e] = m[n][e];
+            sm_l[pc * C::ROWS + 8 * n + 2 * c + e] = l[n][e];
+          }
+      }
+      if (lane == 0) sh.piece[pc] = {s0 + seg.i - ta, seg.b, seg.h, seg.rt, seg.r.nt};
+    }
+    advance(seg, end - ta);
+  }
+  cp_async_wait<0>();
+  __threadfence_block();
+  __syncthreads();
+
+  // --- join the parts of the units that cuts went through -------------------
+  float *cta_part = p.part + (size_t)gridDim.x * AR_WARPS * AR_SLOT<D>;
+  const long long c0 = sh.bound[0], c1 = sh.bound[AR_WARPS];
+  for (int i = 0; i < 2 * AR_WARPS;) {
+    const ArPiece u = sh.piece[i];
+    int j = i + 1;
+    if (u.g0 < 0) {
+      i = j;
+      continue;
+    }
+    while (j < 2 * AR_WARPS && (sh.piece[j].g0 == u.g0 || sh.piece[j].g0 < 0)) ++j;
+    const int n_rows = min(p.RT, rows_of(u.b) * p.G - u.rt * p.RT);
+    const bool here = u.g0 >= c0 && u.g0 + u.nt <= c1;  // no other CTA has tiles of it
+    float *slot = cta_part + (size_t)(2 * cta + (u.g0 >= c0)) * AR_SLOT<D>;
+    for (int f = warp; f < MI * NR; f += AR_WARPS) {
+      const int mi = f / NR, n = f - mi * NR;
+      float mj[2] = {AR_EMPTY, AR_EMPTY}, lj[2] = {0.f, 0.f}, v[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int k = i; k < j; ++k)
+        if (sh.piece[k].g0 >= 0) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) mj[e] = fmaxf(mj[e], sm_m[k * C::ROWS + 8 * n + 2 * c + e]);
+        }
+      for (int k = i; k < j; ++k)
+        if (sh.piece[k].g0 >= 0) {
+          const float4 x =
+              (k & 1) ? reinterpret_cast<const float4 *>(smem + (k >> 1) * C::RING)[f * 32 + lane]
+                      : __ldcg(reinterpret_cast<const float4 *>(
+                                   p.part + (size_t)(cta * AR_WARPS + (k >> 1)) * AR_SLOT<D> + 64) + f * 32 + lane);
+          float w[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            w[e] = exp2_hw(sm_m[k * C::ROWS + 8 * n + 2 * c + e] - mj[e]);
+            lj[e] += sm_l[k * C::ROWS + 8 * n + 2 * c + e] * w[e];
+          }
+          v[0] += x.x * w[0];
+          v[1] += x.y * w[1];
+          v[2] += x.z * w[0];
+          v[3] += x.w * w[1];
+        }
+      if (here) {
+        const float w[2] = {weight(lj[0]), weight(lj[1])};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = scaled(v[k], w[k & 1]);
+        write_frag(v, mi, n, u.b, u.h, u.rt, n_rows);
+      } else {
+        reinterpret_cast<float4 *>(slot + 64)[f * 32 + lane] = make_float4(v[0], v[1], v[2], v[3]);
+        if (mi == 0 && g == 0) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            *reinterpret_cast<float2 *>(slot + 2 * (8 * n + 2 * c + e)) = make_float2(mj[e], lj[e]);
+        }
+      }
+    }
+    if (!here) {
+      // CTAs ca .. cb hold tiles of the unit; ca holds its first.
+      auto cut = [&](int x) {
+        const long long raw = total * ((long long)x * AR_WARPS) / NW;
+        return raw > u.g0 && raw < u.g0 + u.nt ? u.g0 + snap((int)(raw - u.g0), u.nt) : raw;
+      };
+      int ca = cta, cb = cta;
+      while (cut(ca) > u.g0) --ca;
+      while (cb + 1 < P && cut(cb + 1) < u.g0 + u.nt) ++cb;
+      __threadfence();  // this thread's sums, before the count
+      __syncthreads();
+      if (tid == 0) {
+        const bool last = atomicAdd(p.counters + ca, 1u) == (uint32_t)(cb - ca);
+        if (last) p.counters[ca] = 0;
+        sh.last = last;
+      }
+      __syncthreads();
+      if (sh.last) {
+        __threadfence();
+        // slot 2 x + 1 of the CTA that holds the unit's first tile, 2 x of the others
+        auto of = [&](int x) { return cta_part + (size_t)(2 * x + (x == ca)) * AR_SLOT<D>; };
+        for (int f = warp; f < MI * NR; f += AR_WARPS) {
+          const int mi = f / NR, n = f - mi * NR, at = 2 * (8 * n + 2 * c);
+          float mj[2] = {AR_EMPTY, AR_EMPTY}, lj[2] = {0.f, 0.f}, v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+          for (int x = ca; x <= cb; ++x) {
+            const float4 ml = __ldcg(reinterpret_cast<const float4 *>(of(x) + at));
+            mj[0] = fmaxf(mj[0], ml.x);
+            mj[1] = fmaxf(mj[1], ml.z);
+          }
+#pragma unroll 4
+          for (int x = ca; x <= cb; ++x) {
+            const float4 ml = __ldcg(reinterpret_cast<const float4 *>(of(x) + at));
+            const float4 y = __ldcg(reinterpret_cast<const float4 *>(of(x) + 64) + f * 32 + lane);
+            const float w0 = exp2_hw(ml.x - mj[0]), w1 = exp2_hw(ml.z - mj[1]);
+            lj[0] += ml.y * w0;
+            lj[1] += ml.w * w1;
+            v[0] += y.x * w0;
+            v[1] += y.y * w1;
+            v[2] += y.z * w0;
+            v[3] += y.w * w1;
+          }
+          const float w[2] = {weight(lj[0]), weight(lj[1])};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) v[k] = scaled(v[k], w[k & 1]);
+          write_frag(v, mi, n, u.b, u.h, u.rt, n_rows);
+        }
+      }
+      __syncthreads();  // sh.last is written again
+    }
+    i = j;
+  }
+}
+
+size_t attn_rows_scratch_bytes(int D, int num_sms) {
+  return (size_t)(AR_WARPS + 2) * num_sms * (64 + 32 * (size_t)D) * 4;
+}
+
+template <bool Q4, int D, int NR>
+static cudaError_t launch_rows(const ArArgs &p, int num_sms, cudaStream_t s) {
+  static int done[64] = {0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  constexpr int smem = ArCfg<Q4, D, NR>::SMEM;
+  if (dev >= 64 || !done[dev]) {
+    e = cudaFuncSetAttribute(attn_rows_kernel<Q4, D, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) done[dev] = 1;
+  }
+  return launch_pdl(attn_rows_kernel<Q4, D, NR>, dim3((unsigned)num_sms), dim3(AR_THREADS), smem, s, p);
+}
+
+template <bool Q4, int D>
+static cudaError_t launch_rows_nr(const ArArgs &p, int num_sms, cudaStream_t s) {
+  switch ((p.RT + 7) / 8) {
+    case 1: return launch_rows<Q4, D, 1>(p, num_sms, s);
+    case 2: return launch_rows<Q4, D, 2>(p, num_sms, s);
+    case 3: return launch_rows<Q4, D, 3>(p, num_sms, s);
+    default: return launch_rows<Q4, D, 4>(p, num_sms, s);
+  }
+}
+
+cudaError_t launch_attn_rows(const AttnArgs &a, bool q4, float *part, uint32_t *counters, int num_sms, cudaStream_t s) {
+  ArArgs p;
+  p.a = a;
+  p.G = a.Hq / a.H;
+  const long long rq = (long long)a.rows_per_req * p.G;
+  p.n_rt = (int)((rq + 31) / 32);
+  p.RT = (int)((rq + p.n_rt - 1) / p.n_rt);
+  const long long extent = (long long)a.max_blocks * a.block_size;
+  p.extent = (int)(extent < 0x7fffff00ll ? extent : 0x7fffff00ll);
+  p.bs_shift = -1;
+  for (int i = 0; i < 31; ++i)
+    if (a.block_size == 1 << i) p.bs_shift = i;
+  p.part = part;
+  p.counters = counters;
+  if (a.D == 128) return q4 ? launch_rows_nr<true, 128>(p, num_sms, s) : launch_rows_nr<false, 128>(p, num_sms, s);
+  return q4 ? launch_rows_nr<true, 64>(p, num_sms, s) : launch_rows_nr<false, 64>(p, num_sms, s);
+}
+
+}  // namespace mlora

@@ -220,6 +220,11 @@ struct AttnArgs {
   uint16_t *out;
   uint32_t *status;
 };
-cudaError_t launch_attention(const AttnArgs &a, bool q4, int num_sms, cudaStream_t s);
+cudaError_t launch_attn_general(const AttnArgs &a, bool q4, cudaStream_t s);
+// Few rows a request, heads of 64 and 128, 16-byte aligned rows
+// (attn_rows.cu): attn_rows_scratch_bytes of partial sums and one counter per
+// SM (zero between calls).
+size_t attn_rows_scratch_bytes(int D, int num_sms);
+cudaError_t launch_attn_rows(const AttnArgs &a, bool q4, float *part, uint32_t *counters, int num_sms, cudaStream_t s);
 
 }  // namespace mlora
