@@ -732,6 +732,7 @@ static mlora_status attention_impl(const void *y, int M, int ld, int q_col, int 
   if (M == 0) return MLORA_OK;
   uint8_t *ws = (uint8_t *)workspace;
   const bool fast = attn_head_fast(D) && ld % 8 == 0 && q_col % 8 == 0 && aligned(y, 16) && aligned(k, 16) && aligned(v, 16);
+  if (fast && (long long)rows_per_req * (Hq / H) >= 64) return cuda_status(launch_attn_prompt(a, q4, (cudaStream_t)stream));
   if (fast)
     return cuda_status(launch_attn_rows(a, q4, reinterpret_cast<float *>(ws + WS_SCRATCH_OFF),
                                         reinterpret_cast<uint32_t *>(ws + WS_COUNTERS_OFF), sms, (cudaStream_t)stream));

@@ -1,0 +1,40 @@
+// What the attention kernels share: the positions that rows see, and the
+// table look-up.
+#pragma once
+
+#include "common.cuh"
+#include "launch.h"
+
+namespace mlora {
+
+// The positions that rows at p_lo .. p_hi see between them: sinks [0, sink)
+// and [w0, n), w0 rounded down to a tile of TILE positions; the sinks' st tiles
+// come first of nt.
+struct AttnRange {
+  int w0, n, sink, st, nt;
+};
+
+template <int TILE>
+__device__ __forceinline__ AttnRange attn_range(long long p_lo, long long p_hi, int window, int sinks, int extent) {
+  AttnRange r = {0, 0, 0, 0, 0};
+  r.n = (int)min(p_hi + 1, (long long)extent);
+  if (window && p_lo >= window) {
+    r.w0 = (int)min(p_lo - window + 1, (long long)r.n) & ~(TILE - 1);
+    r.sink = min(sinks, r.w0);
+    r.st = (r.sink + TILE - 1) / TILE;
+  }
+  r.nt = r.st + (r.n - r.w0 + TILE - 1) / TILE;
+  return r;
+}
+
+template <int TILE>
+__device__ __forceinline__ int attn_tile_start(const AttnRange &r, int tile) {
+  return tile < r.st ? tile * TILE : r.w0 + (tile - r.st) * TILE;
+}
+
+// r / G by multiplication: magic = ceil(2^32 / G), exact for r < 2^32 / G.
+__device__ __forceinline__ int div_heads(int r, int G, uint32_t magic) {
+  return G == 1 ? r : (int)__umulhi((uint32_t)r, magic);
+}
+
+}  // namespace mlora

@@ -1,0 +1,647 @@
+// Attention for many rows a request (prompts and pieces of them): heads of 64
+// and 128 on the tcgen05 tensor cores, over the bf16 or the 4-bit paged cache.
+//
+// With hundreds of query rows against each cache head the work is 4 D
+// multiply-adds per (row, position) and the bound is the tensor cores.  A CTA
+// takes (request, cache head, 256 query rows): rows are (step, query head of
+// the group) in order, so the heads that share a cache head share its tiles.
+// For each tile of 128 positions and each half of 128 rows
+//   S = Q K^T          operands in shared memory, S in tensor memory;
+//   P = 2^(S - m)      one thread per row, registers, back over S;
+//   O += P V           P from tensor memory, O stays in tensor memory.
+// The halves alternate: the tensor cores work on one while the threads of the
+// other take exponentials.  The running maximum m moves (and O is rescaled,
+// in tensor memory) only when a score exceeds it by 8 in log2 units; until
+// then a tile is one pass over its scores.
+//
+// Warps 0-3 and 4-7 hold the rows of the two halves, warp 8 issues the MMAs,
+// warps 9-11 bring the tiles: a gather of 16-byte pieces through the block
+// table into 128-byte-swizzled rows (K read K-major, V along its rows); over
+// the 4-bit cache they expand codes to fp16 on the way, exactly.
+#include "attn_common.cuh"
+#include "e2m1.cuh"
+#include "prob.cuh"
+
+namespace mlora {
+
+constexpr int AP_TILE = 128;
+constexpr int AP_GROUPS = 4;   // of 32 positions in a tile
+constexpr int AP_LOADERS = 3;  // 12 warps leave 168 registers to a thread, which the scores' threads need
+constexpr int AP_MMA_WARP = 8;
+constexpr int AP_WARPS = 9 + AP_LOADERS;
+constexpr int AP_THREADS = 32 * AP_WARPS;
+constexpr float AP_SLACK = 8.f;
+constexpr float AP_NONE = -__builtin_huge_valf();
+
+template <int D>
+struct ApCfg {
+  static constexpr int BLOCK = AP_TILE * 128;           // 128 rows of 64 elements, 128-byte swizzle
+  static constexpr int OPERAND = BLOCK * (D / 64);      // 128 rows of D elements
+  static constexpr int Q_OFF = 0;                       // two halves
+  static constexpr int K_OFF = 2 * OPERAND;             // two stages
+  static constexpr int V_OFF = 4 * OPERAND;             // two stages
+  static constexpr int BAR_OFF = 6 * OPERAND;
+  static constexpr int SMEM = BAR_OFF + 512 + 1024;     // and the alignment
+};
+
+struct ApShared {
+  uint64_t q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full[2], fin;
+  uint32_t tmem;
+  int abort;
+  uint32_t there[2][AP_GROUPS];  // per V stage: positions whose slot is in the cache
+  int odd[2][AP_GROUPS];         // per V stage: some V that not every row sees is not finite
+};
+static_assert(sizeof(ApShared) <= 512, "ApShared");
+
+struct ApArgs {
+  AttnArgs a;
+  int G;
+  uint32_t G_magic;
+  int extent, bs_shift;
+  int n_rt, halves;  // row tiles per (request, cache head), of halves * 128 rows
+};
+
+__device__ __forceinline__ void ap_cp_async_16(uint32_t dst, const void *src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void ap_cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Wait for the loads whose registers are named, so that no use moves before it.
+__device__ __forceinline__ void tmem_ld_wait32(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_x32(uint32_t taddr, const uint32_t *r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// D[tmem] (+)= A[tmem] * B[smem], 16-bit inputs, fp32 accumulator, one CTA.
+__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                           uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// V's tile as the second product's B operand: 16 positions (K) by D elements
+// (N), N contiguous: rows of 64 elements (128 bytes, swizzled), 8 positions
+// 1024 bytes apart (stride offset), the next 64 elements a block further
+// (leading offset).
+__device__ __forceinline__ uint64_t smem_desc_nmajor_sw128(uint32_t saddr, uint32_t block_bytes) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)(block_bytes >> 4) << 16;  // leading byte offset
+  d |= (uint64_t)(1024 >> 4) << 32;         // stride byte offset
+  d |= (uint64_t)1 << 46;                   // descriptor version
+  d |= (uint64_t)2 << 61;                   // 128-byte swizzle
+  return d;
+}
+
+template <bool F16>
+__host__ __device__ constexpr uint32_t ap_idesc(int N, bool b_n_major) {
+  return (1u << 4) | ((F16 ? 0u : 1u) << 7) | ((F16 ? 0u : 1u) << 10) | ((b_n_major ? 1u : 0u) << 16) |
+         ((uint32_t)(N >> 3) << 17) | ((128u >> 4) << 24);
+}
+
+template <bool F16>
+__device__ __forceinline__ uint32_t ap_pack2(float lo, float hi) {
+  uint32_t r;
+  if (F16)
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t ap_hmul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+template <bool Q4, int D>
+__global__ void __launch_bounds__(AP_THREADS, 1) attn_prompt_kernel(const ApArgs p) {
+  using C = ApCfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = align_smem_1024(smem_raw);
+  ApShared &sh = *reinterpret_cast<ApShared *>(smem + C::BAR_OFF);
+  const AttnArgs &a = p.a;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int T = a.rows_per_req, RT = p.halves * 128;
+  // Later rows see more: they go first.
+  const int per = a.H * a.B;
+  const int rt = p.n_rt - 1 - (int)(blockIdx.x / per);
+  const int h = (int)(blockIdx.x % per) % a.H, b = (int)(blockIdx.x % per) / a.H;
+  const int rq = min(T, a.M - b * T) * p.G, r0 = rt * RT;  // rows of the request, the CTA's first
+  if (r0 >= rq) return;
+  const int n_rows = min(RT, rq - r0);
+
+  grid_dependency_wait();  // y, the cache and the lengths come from the kernels just before
+  const int L = __ldg(a.seq_len + b);
+  const long long p0 = (long long)L + a.t0;
+  const long long p_lo = p0 + div_heads(r0, p.G, p.G_magic), p_hi = p0 + div_heads(r0 + n_rows - 1, p.G, p.G_magic);
+  const AttnRange R = attn_range<AP_TILE>(p_lo, p_hi, a.window, a.sinks, p.extent);
+  const int nt = L < 0 ? 0 : R.nt;
+  if (L >= 0 && tid == 0 && p_hi >= p.extent) raise_status(a.status, MLORA_DEV_BAD_SLOT);
+
+  auto out_row = [&](int r) {  // row r of the request
+    const int t = div_heads(r, p.G, p.G_magic);
+    return a.out + ((size_t)(b * T + t) * a.Hq + h * p.G + r - t * p.G) * D;
+  };
+  if (nt == 0) {  // nothing to see: zeros
+    for (int i = tid; i < n_rows * (D / 8); i += AP_THREADS)
+      reinterpret_cast<uint4 *>(out_row(r0 + i / (D / 8)))[i % (D / 8)] = make_uint4(0, 0, 0, 0);
+    return;
+  }
+
+  const int halves = n_rows > 128 ? 2 : 1;
+  if (tid == 0) {
+    mbar_init(&sh.q_full, 128 * halves);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.k_full[i], AP_GROUPS);
+      mbar_init(&sh.v_full[i], AP_GROUPS);
+      mbar_init(&sh.k_empty[i], 1);
+      mbar_init(&sh.v_empty[i], 1);
+      mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.p_full[i], 128);
+      mbar_init(&sh.o_full[i], 1);
+    }
+    mbar_init(&sh.fin, 1);
+    sh.abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == AP_MMA_WARP) {
+    tmem_alloc(&sh.tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before_sync();
+  block_sync();
+  tc_fence_after_sync();
+  // Kernels that follow may take tensor memory only when this CTA has its own.
+  grid_launch_dependents();
+  const uint32_t tmem = sh.tmem;
+  volatile int *abort = &sh.abort;
+  auto wait = [&](uint64_t *bar, uint32_t parity) {
+    if (mbar_wait_bounded(bar, parity & 1u, abort)) return true;
+    *abort = 1;
+    return false;
+  };
+  // S (and P over it) of half i at column 128 i, O at 256 + 128 i.
+
+  if (warp < 8) {
+    const int half = warp >> 2;
+    if (half < halves) {
+      // --- a row per thread --------------------------------------------------
+      const int row = (warp & 3) * 32 + lane, r = r0 + half * 128 + row;
+      const bool valid = r < rq;
+      const int rc = min(r, rq - 1), t = div_heads(rc, p.G, p.G_magic);
+      const long long pos = p0 + t;
+      const int hi = (int)min(pos, 0x7fffffffll);  // sees j <= hi, j > lo or j < sinks
+      const int lo = a.window ? (int)max(min(pos - a.window, 0x7fffffffll), -1ll) : -1;
+      const int hi_first = __shfl_sync(0xffffffffu, hi, 0), lo_last = __shfl_sync(0xffffffffu, lo, 31);
+      float mul = a.scale_log2;
+      {
+        const uint16_t *src = a.y + (size_t)(b * T + t) * a.ld + a.q_col + (size_t)(h * p.G + rc - t * p.G) * D;
+        uint8_t *dst = smem + C::Q_OFF + half * C::OPERAND + row * 128;
+        float down = 1.f;
+        if (Q4) {
+          // fp16 relative to the row's largest magnitude (a power of two, given
+          // back to the scores): exact but for entries 2^-14 below it.
+          uint32_t mx = 0;
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) {
+            const uint4 v = __ldg(reinterpret_cast<const uint4 *>(src) + i);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mx = max(mx, max(w[k] & 0x7FFFu, (w[k] >> 16) & 0x7FFFu));
+          }
+          const uint32_t e = min(max(mx >> 7, 1u), 253u);
+          down = __uint_as_float((254u - e) << 23);
+          mul *= __uint_as_float(e << 23);
+        }
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          uint4 v = valid ? __ldg(reinterpret_cast<const uint4 *>(src) + i) : make_uint4(0, 0, 0, 0);
+          if (Q4) {
+            uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              w[k] = ap_pack2<true>(__uint_as_float(w[k] << 16) * down, __uint_as_float(w[k] & 0xFFFF0000u) * down);
+            v = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+          *reinterpret_cast<uint4 *>(dst + (i >> 3) * C::BLOCK + ((i & 7) ^ (row & 7)) * 16) = v;
+        }
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(&sh.q_full);
+
+      const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+      const uint32_t ts = tmem + lanes + 128 * half, to = tmem + lanes + 256 + 128 * half;
+      float m = AP_NONE, l = 0.f;
+      bool ok = true;
+      for (int j = 0; j < nt; ++j) {
+        ok = wait(&sh.s_full[half], j) && wait(&sh.v_full[j & 1], j >> 1);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after_sync();
+        const int j0 = attn_tile_start<AP_TILE>(R, j), jl = j0 + AP_TILE - 1;
+        uint32_t there[4];
+        int odd = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          there[i] = sh.there[j & 1][i];
+          odd |= sh.odd[j & 1][i];
+        }
+        const bool edge = (there[0] & there[1] & there[2] & there[3]) != 0xffffffffu || jl > hi_first ||
+                          (a.window && !(j0 > lo_last || jl < a.sinks));
+        auto sees = [&](int jj, uint32_t bits) {
+          const int jp = j0 + jj;
+          return ((bits >> (jj & 31)) & 1u) && jp <= hi && (jp > lo || jp < a.sinks);
+        };
+        uint32_t P[64];
+        float sum = 0.f;
+        // At most two more passes: past 2^27 a score's rounding exceeds the slack.
+        for (int pass = 0; pass < 3; ++pass) {
+          const float base = m == AP_NONE ? 0.f : m;
+          float mx = AP_NONE;
+          sum = 0.f;
+#pragma unroll
+          for (int ch = 0; ch < 4; ++ch) {
+            uint32_t x[32];
+            tmem_ld_x32(ts + 32 * ch, x);
+            tmem_ld_wait32(x);
+            float v[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = fmaf(__uint_as_float(x[i]), mul, -base);
+            if (edge) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (!sees(32 * ch + i, there[ch])) v[i] = AP_NONE;
+            }
+#pragma unroll
+            for (int i = 0; i < 32; ++i) mx = fmaxf(mx, v[i]);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = exp2_hw(v[i]);
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              sum += v[i] + v[i + 1];
+              P[16 * ch + i / 2] = ap_pack2<Q4>(v[i], v[i + 1]);
+            }
+          }
+          const bool far = mx > AP_SLACK || (m == AP_NONE && mx > AP_NONE);
+          if (pass == 2 || !__any_sync(0xffffffffu, far)) break;
+          // Move the maximum of the rows that need it, rescale what is summed so far, take the tile again.
+          float corr = 1.f;
+          if (far) {
+            if (m != AP_NONE) corr = exp2_hw(-mx);
+            m = base + mx;
+            l *= corr;
+          }
+          if (j > 0) {
+#pragma unroll
+            for (int i = 0; i < D; i += 32) {
+              uint32_t o[32];
+              tmem_ld_x32(to + i, o);
+              tmem_ld_wait32(o);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * corr);
+              tmem_st_x32(to + i, o);
+            }
+            tmem_st_wait();
+          }
+        }
+        l += sum;
+        if (odd) {
+          // Values that are not finite and that some rows do not see: the
+          // product would bring 0 times them to those rows.  This tile is added
+          // up here, a position at a time (the MMA warp leaves it out).
+          const float base = m == AP_NONE ? 0.f : m;
+          for (int d0 = 0; d0 < D; d0 += 32) {
+            uint32_t o[32];
+            if (j > 0) {
+              tmem_ld_x32(to + d0, o);
+              tmem_ld_wait32(o);
+            } else {
+#pragma unroll
+              for (int k = 0; k < 32; ++k) o[k] = 0;
+            }
+            for (int jj = 0; jj < AP_TILE; ++jj) {
+              uint32_t s1;
+              tmem_ld_x1(ts + jj, s1);
+              asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(s1) : : "memory");
+              const uint32_t bits = jj < 64 ? (jj < 32 ? there[0] : there[1]) : (jj < 96 ? there[2] : there[3]);
+              if (sees(jj, bits)) {
+                const float w = exp2_hw(fmaf(__uint_as_float(s1), mul, -base));
+                const uint8_t *v = smem + C::V_OFF + (j & 1) * C::OPERAND + (d0 >> 6) * C::BLOCK + jj * 128;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  const uint4 q = *reinterpret_cast<const uint4 *>(v + ((((d0 & 32) >> 3) + k) ^ (jj & 7)) * 16);
+                  const uint32_t e[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) {
+                    const float x0 = Q4 ? f16_lo(e[i]) : __uint_as_float(e[i] << 16);
+                    const float x1 = Q4 ? f16_hi(e[i]) : __uint_as_float(e[i] & 0xFFFF0000u);
+                    o[8 * k + 2 * i] = __float_as_uint(fmaf(w, x0, __uint_as_float(o[8 * k + 2 * i])));
+                    o[8 * k + 2 * i + 1] = __float_as_uint(fmaf(w, x1, __uint_as_float(o[8 * k + 2 * i + 1])));
+                  }
+                }
+              }
+              __syncwarp();
+            }
+            tmem_st_x32(to + d0, o);
+          }
+        } else {
+          tmem_st_x32(ts, P);
+          tmem_st_x32(ts + 32, P + 32);
+        }
+        tmem_st_wait();
+        tc_fence_before_sync();
+        mbar_arrive(&sh.p_full[half]);
+      }
+      if (ok) ok = __all_sync(0xffffffffu, wait(&sh.o_full[half], 0));
+      if (ok) {
+        tc_fence_after_sync();
+        const float w = l != 0.f ? a.v_unit / l : 0.f;
+        uint4 *dst = reinterpret_cast<uint4 *>(out_row(rc));
+#pragma unroll
+        for (int i = 0; i < D; i += 32) {
+          uint32_t o[32];
+          tmem_ld_x32(to + i, o);
+          tmem_ld_wait32(o);
+          if (valid) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              uint32_t x[4];
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                x[q] = w != 0.f ? ap_pack2<false>(__uint_as_float(o[8 * k + 2 * q]) * w, __uint_as_float(o[8 * k + 2 * q + 1]) * w)
+                                : 0u;
+              dst[i / 8 + k] = make_uint4(x[0], x[1], x[2], x[3]);
+            }
+          }
+        }
+        tc_fence_before_sync();
+      }
+    }
+  } else if (warp == AP_MMA_WARP) {
+    // --- the MMAs, issued by lane 0 -------------------------------------------
+    const uint32_t q0 = smem_addr(smem + C::Q_OFF), k0 = smem_addr(smem + C::K_OFF), v0 = smem_addr(smem + C::V_OFF);
+    constexpr uint32_t ID_S = ap_idesc<Q4>(AP_TILE, false), ID_O = ap_idesc<Q4>(D, true);
+    auto scores = [&](int j, int half) {
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks) {
+        const uint32_t off = (ks >> 2) * C::BLOCK + (ks & 3) * 32;
+        mma_bf16_ss(tmem + 128 * half, smem_desc_kmajor_sw128(q0 + half * C::OPERAND + off),
+                    smem_desc_kmajor_sw128(k0 + (j & 1) * C::OPERAND + off), ID_S, ks > 0);
+      }
+      mma_commit(&sh.s_full[half]);
+      if (half == halves - 1) mma_commit(&sh.k_empty[j & 1]);
+    };
+    bool ok = wait(&sh.q_full, 0) && wait(&sh.k_full[0], 0);
+    ok = __all_sync(0xffffffffu, ok);
+    tc_fence_after_sync();
+    if (ok && lane == 0)
+      for (int half = 0; half < halves; ++half) scores(0, half);
+    __syncwarp();
+    for (int j = 0; j < nt && ok; ++j) {
+      for (int half = 0; half < halves && ok; ++half) {
+        ok = wait(&sh.p_full[half], j) && wait(&sh.v_full[j & 1], j >> 1);
+        if (j + 1 < nt) ok = ok && wait(&sh.k_full[(j + 1) & 1], (j + 1) >> 1);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after_sync();
+        if (lane == 0) {
+          const bool odd = sh.odd[j & 1][0] | sh.odd[j & 1][1] | sh.odd[j & 1][2] | sh.odd[j & 1][3];
+          if (!odd) {
+#pragma unroll
+            for (int kk = 0; kk < AP_TILE / 16; ++kk)
+              mma_f16_ts(tmem + 256 + 128 * half, tmem + 128 * half + 8 * kk,
+                         smem_desc_nmajor_sw128(v0 + (j & 1) * C::OPERAND + kk * 2048, C::BLOCK), ID_O, j > 0 || kk > 0);
+          }
+          if (half == halves - 1) mma_commit(&sh.v_empty[j & 1]);
+          if (j + 1 < nt)
+            scores(j + 1, half);
+          else
+            mma_commit(&sh.o_full[half]);
+        }
+        __syncwarp();
+      }
+    }
+    if (!ok) {  // what was issued ends before the tensor memory goes back
+      int never = 0;
+      if (lane == 0) mma_commit(&sh.fin);
+      mbar_wait_bounded(&sh.fin, 0, &never);
+    }
+  } else {
+    // --- the tiles ------------------------------------------------------------
+    // Groups of 32 positions of K of tile 0, V of tile 0, K of tile 1, ... go to
+    // the warps in turn: group x is part x & 3 of half-tile x / 4.
+    const int n_groups = 2 * AP_GROUPS * nt;
+    auto slot_of = [&](int x) {  // of this lane's position; -1: none
+      if (x >= n_groups) return -1;
+      const int j = x >> 3, pos = attn_tile_start<AP_TILE>(R, j) + 32 * (x & 3) + lane;
+      if (pos >= (j < R.st ? R.sink : R.n)) return -1;
+      const int page = p.bs_shift >= 0 ? pos >> p.bs_shift : pos / a.block_size;
+      const int blk = __ldg(a.block_table + (size_t)b * a.max_blocks + page), off = pos - page * a.block_size;
+      if (blk < 0 || blk >= a.num_blocks) {
+        raise_status(a.status, MLORA_DEV_BAD_SLOT);
+        return -1;
+      }
+      return Q4 ? (blk * a.H + h) * a.block_size + off : blk * a.block_size + off;
+    };
+    // Whether some row of the CTA does not see all of tile j.
+    auto partial = [&](int j) {
+      const int j0 = attn_tile_start<AP_TILE>(R, j), jl = j0 + AP_TILE - 1;
+      return jl > p_lo || (a.window && !(j0 > p_hi - a.window || jl < a.sinks));
+    };
+    auto room = [&](int x) {  // the half-tile's place is free
+      const int j = x >> 3;
+      return j < 2 || __all_sync(0xffffffffu, wait(x & 4 ? &sh.v_empty[j & 1] : &sh.k_empty[j & 1], (j >> 1) - 1));
+    };
+    auto arrive = [&](int x) {  // this warp's part of it is there
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(x & 4 ? &sh.v_full[(x >> 3) & 1] : &sh.k_full[(x >> 3) & 1]);
+    };
+    const int w = warp - AP_MMA_WARP - 1;
+    int next = slot_of(w);
+    if (!Q4) {
+      constexpr int CH = D / 8, PER = 32 / CH;  // 16-byte pieces of a row, rows per instruction
+      const int ch = lane & (CH - 1), t0 = lane / CH;
+      const uint32_t stride = (uint32_t)a.H * D * 2;
+      auto finish = [&](int x) {  // the copies of group x have landed
+        const int j = x >> 3;
+        if (x & 4) {
+          __syncwarp();
+          bool odd = false;
+          if (partial(j)) {
+            const uint8_t *v = smem + C::V_OFF + (j & 1) * C::OPERAND + (32 * (x & 3) + lane) * 128;
+            for (int piece = 0; piece < CH; ++piece) {
+              const uint4 q = *reinterpret_cast<const uint4 *>(v + (piece >> 3) * C::BLOCK + (piece & 7) * 16);
+              const uint32_t e[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+              for (int k = 0; k < 4; ++k) odd |= (e[k] & 0x7F80u) == 0x7F80u || (e[k] & 0x7F800000u) == 0x7F800000u;
+            }
+            odd = __any_sync(0xffffffffu, odd);
+          }
+          if (lane == 0) sh.odd[j & 1][x & 3] = odd;
+        }
+        arrive(x);
+      };
+      int x = w;
+      for (; x < n_groups; x += AP_LOADERS) {
+        const int j = x >> 3, slot = next;
+        next = slot_of(x + AP_LOADERS);
+        if (!room(x)) break;
+        const uint32_t there = __ballot_sync(0xffffffffu, slot >= 0);
+        if ((x & 4) && lane == 0) sh.there[j & 1][x & 3] = there;
+        const uint8_t *src = static_cast<const uint8_t *>(x & 4 ? a.v : a.k) + (size_t)h * D * 2 + ch * 16;
+        const uint32_t dst = smem_addr(smem + (x & 4 ? C::V_OFF : C::K_OFF) + (j & 1) * C::OPERAND) + (ch >> 3) * C::BLOCK;
+#pragma unroll
+        for (int i = 0; i < 32 / PER; ++i) {
+          const int t = i * PER + t0, row = 32 * (x & 3) + t;
+          const int s = __shfl_sync(0xffffffffu, slot, t);
+          ap_cp_async_16(dst + row * 128 + ((ch & 7) ^ (row & 7)) * 16, src + (size_t)(uint32_t)max(s, 0) * stride, s >= 0);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        if (x >= 2 * AP_LOADERS) {  // two groups of this warp stay in flight
+          ap_cp_async_wait<2>();
+          finish(x - 2 * AP_LOADERS);
+        }
+      }
+      if (x >= n_groups) {
+        if (x >= 2 * AP_LOADERS) {
+          ap_cp_async_wait<1>();
+          finish(x - 2 * AP_LOADERS);
+        }
+        ap_cp_async_wait<0>();
+        if (x >= AP_LOADERS) finish(x - AP_LOADERS);
+      }
+      ap_cp_async_wait<0>();
+    } else {
+      // Four lanes (D = 128) or two (D = 64) to a position, 16 bytes of codes
+      // (32 elements, two scales) each.
+      constexpr int CL = D / 32, PER = 32 / CL, NI = 32 / PER;
+      const int cl = lane & (CL - 1), t0 = lane / CL;
+      for (int x = w; x < n_groups; x += AP_LOADERS) {
+        const int j = x >> 3, slot = next;
+        next = slot_of(x + AP_LOADERS);
+        const uint8_t *codes = static_cast<const uint8_t *>(x & 4 ? a.v : a.k) + cl * 16;
+        const uint8_t *scales = (x & 4 ? a.vs : a.ks) + cl * 2;
+        uint4 q[NI];
+        uint32_t sc[NI];
+        bool odd = false;
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+          const int s = __shfl_sync(0xffffffffu, slot, i * PER + t0);
+          q[i] = make_uint4(0, 0, 0, 0);
+          sc[i] = 0;
+          if (s >= 0) {
+            q[i] = __ldg(reinterpret_cast<const uint4 *>(codes + (size_t)s * (D / 2)));
+            sc[i] = __ldg(reinterpret_cast<const unsigned short *>(scales + (size_t)s * (D / 16)));
+          }
+        }
+        if (!room(x)) break;
+        const uint32_t there = __ballot_sync(0xffffffffu, slot >= 0);
+        uint8_t *dst = smem + (x & 4 ? C::V_OFF : C::K_OFF) + (j & 1) * C::OPERAND;
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+          const int row = 32 * (x & 3) + i * PER + t0;
+          odd |= (sc[i] & 0x7Fu) == 0x7Fu || (sc[i] & 0x7F00u) == 0x7F00u;
+          const uint32_t two = e4m3x2_to_f16(sc[i]);
+          const uint32_t s01[2] = {__byte_perm(two, two, 0x1010), __byte_perm(two, two, 0x3232)};
+          const uint32_t words[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+          uint4 o[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t f[4];
+            e2m1x8_to_f16(words[k], f);
+            const uint32_t s = s01[k >> 1];
+            o[k] = make_uint4(ap_hmul2(f[0], s), ap_hmul2(f[1], s), ap_hmul2(f[2], s), ap_hmul2(f[3], s));
+          }
+          // Pieces 4 cl .. 4 cl + 3 of the row; lanes of the upper 64 elements
+          // start two pieces later, so that eight lanes' stores differ in bank.
+          uint8_t *at = dst + (cl >> 1) * C::BLOCK + row * 128;
+          const bool turn = cl & 2;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int piece = 4 * (cl & 1) + (turn ? k ^ 2 : k);
+            *reinterpret_cast<uint4 *>(at + (piece ^ (row & 7)) * 16) = turn ? o[k ^ 2] : o[k];
+          }
+        }
+        if (x & 4) {
+          odd = __any_sync(0xffffffffu, odd) && partial(j);
+          if (lane == 0) {
+            sh.odd[j & 1][x & 3] = odd;
+            sh.there[j & 1][x & 3] = there;
+          }
+        }
+        arrive(x);
+      }
+    }
+  }
+  tc_fence_before_sync();
+  block_sync();
+  if (warp == AP_MMA_WARP) {
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, 512);
+  }
+  if (tid == 0 && sh.abort) raise_status(a.status, MLORA_DEV_TIMEOUT);
+}
+
+template <bool Q4, int D>
+static cudaError_t launch_prompt(const ApArgs &p, cudaStream_t s) {
+  static int done[64] = {0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  constexpr int smem = ApCfg<D>::SMEM;
+  if (dev >= 64 || !done[dev]) {
+    e = cudaFuncSetAttribute(attn_prompt_kernel<Q4, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) done[dev] = 1;
+  }
+  const long long grid = (long long)p.n_rt * p.a.H * p.a.B;
+  return launch_pdl(attn_prompt_kernel<Q4, D>, dim3((unsigned)grid), dim3(AP_THREADS), smem, s, p);
+}
+
+cudaError_t launch_attn_prompt(const AttnArgs &a, bool q4, cudaStream_t s) {
+  ApArgs p;
+  p.a = a;
+  p.G = a.Hq / a.H;
+  p.G_magic = (uint32_t)(((1ull << 32) + p.G - 1) / p.G);
+  const long long extent = (long long)a.max_blocks * a.block_size;
+  p.extent = (int)(extent < 0x7fffff00ll ? extent : 0x7fffff00ll);
+  p.bs_shift = -1;
+  for (int i = 0; i < 31; ++i)
+    if (a.block_size == 1 << i) p.bs_shift = i;
+  const long long rq = (long long)a.rows_per_req * p.G;
+  p.halves = rq > 128 ? 2 : 1;
+  p.n_rt = (int)((rq + 128 * p.halves - 1) / (128 * p.halves));
+  if (a.D == 128) return q4 ? launch_prompt<true, 128>(p, s) : launch_prompt<false, 128>(p, s);
+  return q4 ? launch_prompt<true, 64>(p, s) : launch_prompt<false, 64>(p, s);
+}
+
+}  // namespace mlora

@@ -10,8 +10,8 @@
 // or 32 positions) of all units, in order, are cut into equal contiguous
 // shares, one per warp (8 warps to a CTA, one CTA per SM), so mixed lengths
 // balance by themselves; every CTA finds its shares from the lengths on the
-// device.  A cut that would leave less than AR_SNAP tiles of a unit on one side
-// moves to the unit's end.  A warp has its own ring of asynchronous copies,
+// device.  A cut that would leave only a few tiles of a unit on one side
+// (less than 3 and a quarter of a share) moves to the unit's end.  A warp has its own ring of asynchronous copies,
 // query rows, running maximum, sums and output accumulators, and there is no
 // barrier until all tiles are done: a unit within a warp's share is written
 // from registers.  What is left at the end are the units that cuts went
@@ -33,26 +33,27 @@
 // the first product and of the positions in the second is free as long as
 // both operands agree, and is chosen so that a lane's 16 bytes of K codes and
 // 8 bytes of V codes are contiguous.
-#include "common.cuh"
+#include "attn_common.cuh"
 #include "e2m1.cuh"
-#include "launch.h"
 #include "prob.cuh"
 
 namespace mlora {
 
-constexpr int AR_WARPS = 8;
-constexpr int AR_THREADS = 32 * AR_WARPS;
-constexpr float AR_EMPTY = -3.402823466e38f;  // the maximum of nothing: any score replaces it
+// Warps of a CTA (one CTA per SM): as many as registers and rings allow.
+constexpr int ar_warps(bool q4, int nr) { return nr == 1 ? (q4 ? 16 : 12) : nr == 2 && !q4 ? 10 : 8; }
+constexpr int AR_MAX_WARPS = 16;
+constexpr float AR_EMPTY = -3.402823466e38f;  // the maximum of a part in which a row saw nothing
 constexpr float AR_SLACK = 8.f;               // log2 units a score may exceed the running maximum by
 
-constexpr int AR_SNAP = 3;                    // tiles
-constexpr int AR_MIN_TILES = 2;               // tiles a warp gets at least, on average
+constexpr int AR_MIN_TILES = 4;               // tiles per warp below which a unit is not spread over CTAs
 
 template <bool Q4, int D, int NR>
 struct ArCfg {
-  static constexpr int TILE = Q4 && NR < 4 ? 32 : 16;  // positions a warp takes at a time (16: registers)
+  static constexpr int WARPS = ar_warps(Q4, NR);
+  static constexpr int THREADS = 32 * WARPS;
+  static constexpr int TILE = Q4 && NR < 3 ? 32 : 16;  // positions a warp takes at a time (16: registers)
   static constexpr int MT = TILE / 16;
-  static constexpr int STAGES = Q4 ? 128 / TILE : 2;
+  static constexpr int STAGES = Q4 ? (NR == 1 ? 2 : 96 / TILE) : 2;
   static constexpr int KROW = Q4 ? D / 2 : D * 2;  // bytes of a position's row
   static constexpr int SROW = Q4 ? D / 16 : 0;     // bytes of its scales
   static constexpr int V_OFF = TILE * KROW;
@@ -61,16 +62,17 @@ struct ArCfg {
   static constexpr int STAGE_BYTES = VS_OFF + TILE * SROW;
   static constexpr int ROWS = 8 * NR;
   static constexpr int FRAG = D / 16 * NR * 32;    // float4 of a warp's accumulators
-  static constexpr int RING = STAGES * STAGE_BYTES;
-  static_assert(RING >= FRAG * 16, "a warp's accumulators go where its ring was");
+  // (the accumulators go where the ring was)
+  static constexpr int RING = STAGES * STAGE_BYTES > FRAG * 16 ? STAGES * STAGE_BYTES : FRAG * 16;
   static constexpr int QBYTES = ROWS * D * 2;
-  static constexpr int Q_OFF = AR_WARPS * RING;
-  static constexpr int QMUL_OFF = Q_OFF + AR_WARPS * QBYTES;
-  static constexpr int M_OFF = QMUL_OFF + AR_WARPS * ROWS * 4;      // [2 AR_WARPS][ROWS]
-  static constexpr int L_OFF = M_OFF + 2 * AR_WARPS * ROWS * 4;
-  static constexpr int MASK_OFF = L_OFF + 2 * AR_WARPS * ROWS * 4;  // [AR_WARPS][STAGES]
-  static constexpr int MISC_OFF = MASK_OFF + AR_WARPS * STAGES * 4;
-  static constexpr int SMEM = MISC_OFF + 1024;
+  static constexpr int Q_OFF = WARPS * RING;
+  static constexpr int QMUL_OFF = Q_OFF + WARPS * QBYTES;
+  static constexpr int M_OFF = QMUL_OFF + WARPS * ROWS * 4;      // [2 WARPS][ROWS]
+  static constexpr int L_OFF = M_OFF + 2 * WARPS * ROWS * 4;
+  static constexpr int X_OFF = L_OFF + 2 * WARPS * ROWS * 4;        // [2 WARPS][ROWS]
+  static constexpr int MASK_OFF = X_OFF + 2 * WARPS * ROWS * 4;     // [WARPS][STAGES]
+  static constexpr int MISC_OFF = MASK_OFF + WARPS * STAGES * 4;
+  static constexpr int SMEM = MISC_OFF + 2048;
 };
 
 // A part of a unit that a warp computed: the warp's last tiles (their sums in
@@ -80,25 +82,20 @@ struct ArPiece {
   int b, h, rt, nt;
 };
 struct ArShared {
-  long long bound[AR_WARPS + 1];            // the warps' cuts, counted over all units
-  int at_b[AR_WARPS + 1], at_u[AR_WARPS + 1], at_tile[AR_WARPS + 1];
-  long long sums[AR_WARPS];
-  ArPiece piece[2 * AR_WARPS];              // in order: warp 0's first tiles, warp 0's last, ...
-  int last;
+  long long bound[AR_MAX_WARPS + 1];        // the warps' cuts, counted over all units
+  int at_b[AR_MAX_WARPS + 1], at_u[AR_MAX_WARPS + 1], at_tile[AR_MAX_WARPS + 1];
+  long long sums[AR_MAX_WARPS];
+  int used[AR_MAX_WARPS];
+  ArPiece piece[2 * AR_MAX_WARPS];          // in order: warp 0's first tiles, warp 0's last, ...
+  int last[2], ca[2], cb[2];                // units shared with other CTAs: whether to join them, which CTAs
 };
-static_assert(sizeof(ArShared) <= 1024, "ArShared");
-
-// The positions that some row of a request sees: sinks [0, sink) and
-// [w0, n), w0 rounded down to a tile; tiles of the sinks come first.
-struct ArRange {
-  int w0, n, sink, st, nt;
-};
+static_assert(sizeof(ArShared) <= 2048, "ArShared");
 
 // A place in the flattened list of tiles.
 struct ArCursor {
   int i;  // tiles past the warp's first
   int b, h, rt, tile;
-  ArRange r;
+  AttnRange r;
 };
 
 __device__ __forceinline__ void cp_async_16(uint32_t dst, const void *src, bool there) {
@@ -205,6 +202,7 @@ __device__ __forceinline__ int q4_v_off128(int t, int g) {
 struct ArArgs {
   AttnArgs a;
   int G, n_rt, RT;   // query heads per cache head; row tiles per (request, head), rows in each
+  uint32_t G_magic;  // ceil(2^32 / G)
   int extent;        // positions that a block table reaches
   int bs_shift;      // log2 of the page size, or -1
   float *part;       // sums of units in parts: a slot per warp, then two per CTA (AR_SLOT floats each:
@@ -216,91 +214,103 @@ template <int D>
 constexpr size_t AR_SLOT = 64 + 32 * D;
 
 template <bool Q4, int D, int NR>
-__global__ void __launch_bounds__(AR_THREADS, 1) attn_rows_kernel(const ArArgs p) {
+__global__ void __launch_bounds__(ArCfg<Q4, D, NR>::THREADS, 1) attn_rows_kernel(const ArArgs p) {
   using C = ArCfg<Q4, D, NR>;
-  constexpr int TILE = C::TILE, MT = C::MT, S = C::STAGES, KS = D / 16, MI = D / 16, GD = D / 8;
-  extern __shared__ __align__(128) uint8_t smem[];
+  constexpr int WARPS = C::WARPS, THREADS = C::THREADS, TILE = C::TILE, MT = C::MT, S = C::STAGES, KS = D / 16, MI = D / 16, GD = D / 8;
+  extern __shared__ __align__(1024) uint8_t smem[];
   const AttnArgs &a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
   const int cta = blockIdx.x, T = a.rows_per_req, U = a.H * p.n_rt;
   float *qmul = reinterpret_cast<float *>(smem + C::QMUL_OFF) + warp * C::ROWS;
   float *sm_m = reinterpret_cast<float *>(smem + C::M_OFF);
   float *sm_l = reinterpret_cast<float *>(smem + C::L_OFF);
+  float *sm_x = reinterpret_cast<float *>(smem + C::X_OFF);
   uint32_t *vmask = reinterpret_cast<uint32_t *>(smem + C::MASK_OFF);
   ArShared &sh = *reinterpret_cast<ArShared *>(smem + C::MISC_OFF);
   const uint32_t ring = smem_addr(smem) + warp * C::RING;
   uint8_t *qsmem = smem + C::Q_OFF + warp * C::QBYTES;
-  const uint32_t qf = smem_addr(qsmem) + lane * 8;
+  const uint32_t qf = smem_addr(qsmem) + lane * 16;  // fragments of two steps of 16 side by side
 
   grid_launch_dependents();
   grid_dependency_wait();  // y, the cache and the lengths come from the kernels just before
 
+  auto per_head = [&](int r) { return div_heads(r, p.G, p.G_magic); };
   auto rows_of = [&](int b) { return min(T, a.M - b * T); };  // rows of request b in this pass
-  auto range_of = [&](int b) {
-    ArRange r = {0, 0, 0, 0, 0};
+  auto range_of = [&](int b) {  // the positions that request b's rows see
     const int tb = rows_of(b);
     const int L = b < a.B && tb > 0 ? __ldg(a.seq_len + b) : -1;
-    if (L < 0) return r;
-    const long long p0 = (long long)L + a.t0, last = p0 + tb - 1;
-    r.n = (int)min(last + 1, (long long)p.extent);
-    if (a.window && p0 >= a.window) {
-      r.w0 = (int)min(p0 - a.window + 1, (long long)r.n) & ~(TILE - 1);
-      r.sink = min(a.sinks, r.w0);
-      r.st = (r.sink + TILE - 1) / TILE;
-    }
-    r.nt = r.st + (r.n - r.w0 + TILE - 1) / TILE;
-    return r;
+    if (L < 0) return AttnRange{0, 0, 0, 0, 0};
+    const long long p0 = (long long)L + a.t0;
+    return attn_range<TILE>(p0, p0 + tb - 1, a.window, a.sinks, p.extent);
   };
 
   // Requests that see nothing: zeros.  Rows past the table's reach: status.
-  for (int b = cta; b < a.B; b += gridDim.x) {
-    const int tb = rows_of(b);
-    if (tb <= 0) break;
-    const ArRange r = range_of(b);
-    if (r.nt == 0) {
-      uint4 *dst = reinterpret_cast<uint4 *>(a.out + (size_t)b * T * a.Hq * D);
-      const size_t n = (size_t)tb * a.Hq * D / 8;
-      for (size_t i = tid; i < n; i += AR_THREADS) dst[i] = make_uint4(0, 0, 0, 0);
+  auto unseen = [&]() {
+    for (int b = cta; b < a.B; b += gridDim.x) {
+      const int tb = rows_of(b);
+      if (tb <= 0) break;
+      if (range_of(b).nt == 0) {
+        uint4 *dst = reinterpret_cast<uint4 *>(a.out + (size_t)b * T * a.Hq * D);
+        const size_t n = (size_t)tb * a.Hq * D / 8;
+        for (size_t i = tid; i < n; i += THREADS) dst[i] = make_uint4(0, 0, 0, 0);
+      }
+      if (tid == 0) {
+        const int L = __ldg(a.seq_len + b);
+        if (L >= 0 && (long long)L + a.t0 + tb > p.extent) raise_status(a.status, MLORA_DEV_BAD_SLOT);
+      }
     }
-    if (tid == 0) {
-      const int L = __ldg(a.seq_len + b);
-      if (L >= 0 && (long long)L + a.t0 + tb > p.extent) raise_status(a.status, MLORA_DEV_BAD_SLOT);
-    }
-  }
+  };
 
   // All tiles, the CTAs among which they are cut, and this CTA's cuts.
   long long total = 0;
-  for (int base = 0; base < a.B; base += AR_THREADS) {
-    long long v = base + tid < a.B ? range_of(base + tid).nt : 0;
+  int used = 0;  // requests with tiles
+  const int nt0 = tid < a.B ? range_of(tid).nt : 0;
+  for (int base = 0; base < a.B; base += THREADS) {
+    long long v = base == 0 ? nt0 : base + tid < a.B ? range_of(base + tid).nt : 0;
+    used += __popc(__ballot_sync(0xffffffffu, v > 0));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     total += v;
   }
-  if (lane == 0) sh.sums[warp] = total;
-  if (tid < 2 * AR_WARPS) sh.piece[tid].g0 = -1;
+  if (lane == 0) {
+    sh.sums[warp] = total;
+    sh.used[warp] = used;
+  }
+  if (tid < 2 * WARPS) sh.piece[tid].g0 = -1;
   __syncthreads();
   total = 0;
+  used = 0;
 #pragma unroll
-  for (int w = 0; w < AR_WARPS; ++w) total += sh.sums[w];
+  for (int w = 0; w < WARPS; ++w) {
+    total += sh.sums[w];
+    used += sh.used[w];
+  }
   total *= U;
-  if (total == 0) return;
-  // A CTA's share is at least 16 tiles (or all there are): wider than two
-  // moved cuts, so that no CTA is left without tiles.
-  const long long want = max(total / (AR_WARPS * AR_MIN_TILES), 1ll);
-  const int P = (int)min((long long)gridDim.x, want);
-  const int NW = P * AR_WARPS;
-  if (cta >= P) return;
+  // A CTA per unit while they are few and short: a unit that one CTA holds
+  // needs no second join.
+  const long long wide = max(total / (WARPS * AR_MIN_TILES), (long long)used * U);
+  const int P = (int)min((long long)gridDim.x, wide);
+  if (cta >= P) {
+    unseen();
+    return;
+  }
+  // Cut x (of P * WARPS) before it is moved.
+  const bool small = total < (1ll << 31);
+  const long long quot = small ? (long long)((uint32_t)total / (uint32_t)(P * WARPS)) : total / (P * WARPS);
+  const int rest = (int)(total - quot * (P * WARPS));
+  auto raw_cut = [&](int x) { return quot * x + (uint32_t)(rest * x) / (uint32_t)(P * WARPS); };
+  const int near = (int)min(quot / 4, 1ll << 20) + 3;
   // Where the cut at `o` of a unit's nt tiles goes.
-  auto snap = [](int o, int nt) {
-    if (o < AR_SNAP || nt - o < AR_SNAP) return 2 * o < nt ? 0 : nt;
+  auto snap = [&](int o, int nt) {
+    if (o < near || nt - o < near) return 2 * o < nt ? 0 : nt;
     return o;
   };
-  __syncthreads();  // sums are written again
+  long long *ends = reinterpret_cast<long long *>(smem);  // per request: tiles (of one unit each) up to its end
   {
     long long before = 0;
-    for (int base = 0; base < a.B; base += AR_THREADS) {
-      const int nt = base + tid < a.B ? range_of(base + tid).nt : 0;
-      long long v = nt;
+    for (int base = 0; base < a.B; base += THREADS) {
+      __syncthreads();  // sums are written again
+      long long v = base == 0 ? nt0 : base + tid < a.B ? range_of(base + tid).nt : 0;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const long long u = __shfl_up_sync(0xffffffffu, v, o);
@@ -308,29 +318,37 @@ __global__ void __launch_bounds__(AR_THREADS, 1) attn_rows_kernel(const ArArgs p
       }
       if (lane == 31) sh.sums[warp] = v;
       __syncthreads();
-      long long off = before, all = 0;
+      long long off = before, all = before;
 #pragma unroll
-      for (int w = 0; w < AR_WARPS; ++w) {
+      for (int w = 0; w < WARPS; ++w) {
         if (w < warp) off += sh.sums[w];
         all += sh.sums[w];
       }
-      const long long lo = (off + v - nt) * U, hi = (off + v) * U;
-      for (int w = 0; w <= AR_WARPS; ++w) {
-        const long long raw = total * (cta * AR_WARPS + w) / NW;
-        if (lo <= raw && raw < hi) {
-          const int u = (int)((raw - lo) / nt);
-          const int o = snap((int)(raw - lo - (long long)u * nt), nt);
-          sh.at_b[w] = base + tid;
-          sh.at_u[w] = u;
-          sh.at_tile[w] = o;
-          sh.bound[w] = lo + (long long)u * nt + o;
-        } else if (raw == total && hi == total && nt > 0) {
-          sh.bound[w] = total;
+      ends[tid] = off + v;
+      __syncthreads();
+      if (tid <= WARPS) {
+        const long long raw = raw_cut(cta * WARPS + tid);
+        if (raw == total) {
+          sh.bound[tid] = total;
+        } else if (before * U <= raw && raw < all * U) {
+          int x = 0;  // the first request that ends past the cut
+#pragma unroll
+          for (int step = THREADS > 256 ? 256 : THREADS > 128 ? 128 : 64; step > 0; step >>= 1)
+            if (x + step <= THREADS && ends[x + step - 1] * U <= raw) x += step;
+          const long long start = x > 0 ? ends[x - 1] : before;
+          const int nt = (int)(ends[x] - start);
+          const long long in = raw - start * U;
+          const int u = in < (1ll << 31) ? (int)((uint32_t)in / (uint32_t)nt) : (int)(in / nt);
+          const int o = snap((int)(in - (long long)u * nt), nt);
+          sh.at_b[tid] = base + x;
+          sh.at_u[tid] = u;
+          sh.at_tile[tid] = o;
+          sh.bound[tid] = start * U + (long long)u * nt + o;
         }
       }
-      before += all;
-      __syncthreads();
+      before = all;
     }
+    __syncthreads();
   }
   const long long s0 = sh.bound[warp];
   const int count = (int)(sh.bound[warp + 1] - s0);
@@ -351,9 +369,6 @@ __global__ void __launch_bounds__(AR_THREADS, 1) attn_rows_kernel(const ArArgs p
       if (x.b >= a.B) x.i = count;  // (not reached: the share ends within the tiles)
     }
   };
-  auto tile_start = [&](const ArRange &r, int tile) {
-    return tile < r.st ? tile * TILE : r.w0 + (tile - r.st) * TILE;
-  };
 
   ArCursor seg = {0, 0, 0, 0, 0, {0, 0, 0, 0, 0}};  // the segment (a unit's tiles within the share) being computed
   if (count > 0) {
@@ -366,15 +381,12 @@ __global__ void __launch_bounds__(AR_THREADS, 1) attn_rows_kernel(const ArArgs p
   }
 
   // --- loads ---------------------------------------------------------------
-  ArCursor nx = seg;  // the next tile this warp will ask for
-  int n_blk = -1, n_off = 0;
-  bool n_in = false;
   // The page of each of the next tile's positions, asked for ahead of the copies.
-  auto look_up = [&]() {
+  auto look_up = [&](const ArCursor &nx, int &n_blk, int &n_off, bool &n_in) {
     n_in = false;
     n_blk = -1;
     if (nx.i < count) {
-      const int j = tile_start(nx.r, nx.tile) + (lane & (TILE - 1));
+      const int j = attn_tile_start<TILE>(nx.r, nx.tile) + (lane & (TILE - 1));
       n_in = j < (nx.tile < nx.r.st ? nx.r.sink : nx.r.n);
       if (n_in) {
         const int page = p.bs_shift >= 0 ? j >> p.bs_shift : j / a.block_size;
@@ -383,7 +395,7 @@ __global__ void __launch_bounds__(AR_THREADS, 1) attn_rows_kernel(const ArArgs p
       }
     }
   };
-  auto issue = [&](int stage) {
+  auto copy = [&](int stage, const ArCursor &nx, int n_blk, int n_off, bool n_in) {
     if (nx.i < count) {
       int slot = -1;
       if (n_in) {
@@ -397,13 +409,15 @@ __global__ void __launch_bounds__(AR_THREADS, 1) attn_rows_kernel(const ArArgs p
       const uint32_t dst = ring + stage * C::STAGE_BYTES;
       constexpr int CH = C::KROW / 16;           // 16-byte pieces of a row
       constexpr int PER = 32 / CH;               // rows per instruction
-      const int ch = lane & (CH - 1);
+      const int ch = lane & (CH - 1), t0 = lane / CH;
+      const uint32_t stride = Q4 ? C::KROW : (uint32_t)a.H * C::KROW;
+      const size_t in_row = (Q4 ? 0 : (size_t)nx.h * C::KROW) + ch * 16;
+      const uint8_t *kp = static_cast<const uint8_t *>(a.k) + in_row, *vp = static_cast<const uint8_t *>(a.v) + in_row;
 #pragma unroll
       for (int i = 0; i < TILE / PER; ++i) {
-        const int t = i * PER + lane / CH;
+        const int t = i * PER + t0;
         const int s = __shfl_sync(0xffffffffu, slot, t);
-        const size_t row = Q4 ? (size_t)max(s, 0) : (size_t)max(s, 0) * a.H + nx.h;
-        const size_t off = row * C::KROW + ch * 16;
+        const size_t off = (size_t)(uint32_t)max(s, 0) * stride;
         uint32_t ko, vo;
         if (Q4) {
           ko = ((t & 16) + q4_row_of(t & 15)) * C::KROW + ch * 16;
@@ -411,8 +425,8 @@ __global__ void __launch_bounds__(AR_THREADS, 1) attn_rows_kernel(const ArArgs p
         } else {
           ko = vo = t * C::KROW + (ch ^ (t & 7)) * 16;
         }
-        cp_async_16(dst + ko, static_cast<const uint8_t *>(a.k) + off, s >= 0);
-        cp_async_16(dst + C::V_OFF + vo, static_cast<const uint8_t *>(a.v) + off, s >= 0);
+        cp_async_16(dst + ko, kp + off, s >= 0);
+        cp_async_16(dst + C::V_OFF + vo, vp + off, s >= 0);
       }
       if (Q4 && lane < TILE) {
         const size_t off = (size_t)max(slot, 0) * C::SROW;
@@ -420,24 +434,25 @@ __global__ void __launch_bounds__(AR_THREADS, 1) attn_rows_kernel(const ArArgs p
                                          slot >= 0);
         cp_async_small<Q4 ? C::SROW : 4>(dst + C::VS_OFF + lane * C::SROW, a.vs + off, slot >= 0);
       }
-      advance(nx, 1);
-      look_up();
     }
     cp_async_commit();
   };
 
   // --- query rows: the warp's own, as the operand's fragments --------------
-  auto load_q = [&](const ArCursor &x, int n_rows) {
-    uint2 qv[C::ROWS];  // a lane holds elements 4 lane .. + 3 of every row
+  // A lane holds elements 4 lane .. + 3 of every row.
+  auto fetch_q = [&](const ArCursor &x, uint2 (&qv)[C::ROWS]) {
+    const int n_rows = min(p.RT, rows_of(x.b) * p.G - x.rt * p.RT);
 #pragma unroll
     for (int lr = 0; lr < C::ROWS; ++lr) {
       qv[lr] = make_uint2(0, 0);
       if (lr < n_rows && 4 * lane < D) {
-        const int r = x.rt * p.RT + lr, t = r / p.G;
+        const int r = x.rt * p.RT + lr, t = per_head(r);
         const uint16_t *src = a.y + (size_t)(x.b * T + t) * a.ld + a.q_col + (size_t)(x.h * p.G + r - t * p.G) * D;
         qv[lr] = *reinterpret_cast<const uint2 *>(src + 4 * lane);
       }
     }
+  };
+  auto store_q = [&](const uint2 (&qv)[C::ROWS]) {
     __syncwarp();  // the rows before these have been read by every lane
 #pragma unroll
     for (int lr = 0; lr < C::ROWS; ++lr) {
@@ -456,13 +471,13 @@ __global__ void __launch_bounds__(AR_THREADS, 1) attn_rows_kernel(const ArArgs p
           f.x = pack2<true>(__uint_as_float(qv[lr].x << 16) * down, __uint_as_float(qv[lr].x & 0xFFFF0000u) * down);
           f.y = pack2<true>(__uint_as_float(qv[lr].y << 16) * down, __uint_as_float(qv[lr].y & 0xFFFF0000u) * down);
           const int cc = lane / KS, ks = lane % KS;  // elements 4 KS cc + 4 ks ..
-          *reinterpret_cast<uint2 *>(qsmem + ((ks * NR + n) * 32 + row * 4 + cc) * 8) = f;
+          *reinterpret_cast<uint2 *>(qsmem + ((ks / 2 * NR + n) * 32 + row * 4 + cc) * 16 + (ks & 1) * 8) = f;
         }
       } else if (4 * lane < D) {
         const int ks = lane >> 2, q = lane & 3, c0 = 2 * (q & 1);
-        uint8_t *f = qsmem + ((ks * NR + n) * 32 + row * 4 + c0) * 8 + (q >> 1) * 4;
+        uint8_t *f = qsmem + ((ks / 2 * NR + n) * 32 + row * 4 + c0) * 16 + (ks & 1) * 8 + (q >> 1) * 4;
         *reinterpret_cast<uint32_t *>(f) = qv[lr].x;
-        *reinterpret_cast<uint32_t *>(f + 8) = qv[lr].y;
+        *reinterpret_cast<uint32_t *>(f + 16) = qv[lr].y;
       }
     }
     __syncwarp();
@@ -470,7 +485,7 @@ __global__ void __launch_bounds__(AR_THREADS, 1) attn_rows_kernel(const ArArgs p
 
   // --- outputs --------------------------------------------------------------
   auto row_ptr = [&](int b, int h, int rt, int lr) {
-    const int r = rt * p.RT + lr, t = r / p.G;
+    const int r = rt * p.RT + lr, t = per_head(r);
     return a.out + ((size_t)(b * T + t) * a.Hq + h * p.G + r - t * p.G) * D;
   };
   // 16 elements of D (accumulator group mi) of rows 8n .. 8n + 7 from the lanes' fragments.
@@ -496,9 +511,54 @@ __global__ void __launch_bounds__(AR_THREADS, 1) attn_rows_kernel(const ArArgs p
   // A row that saw nothing is zeros, whatever multiplied its weights of 0.
   auto scaled = [](float v, float w) { return w != 0.f ? v * w : 0.f; };
 
-  look_up();
+  // Rows 8n .. 8n + 7 whole, from their accumulators and sums of weights.
+  auto write_rows = [&](float (&v)[MI][4], const float (&l)[2], int n, int b, int h, int rt, int n_rows) {
+    const float w[2] = {weight(l[0]), weight(l[1])};
+    if (Q4) {
+      // A lane's elements of a row are D/8 in a run.
 #pragma unroll
-  for (int s = 0; s < S; ++s) issue(s);
+      for (int e = 0; e < 2; ++e) {
+        const int lr = 8 * n + 2 * c + e;
+        uint32_t x[MI];
+#pragma unroll
+        for (int mi = 0; mi < MI; ++mi) x[mi] = pack2<false>(scaled(v[mi][e], w[e]), scaled(v[mi][2 + e], w[e]));
+        if (lr < n_rows) {
+          uint4 *dst = reinterpret_cast<uint4 *>(row_ptr(b, h, rt, lr) + GD * g);
+#pragma unroll
+          for (int k = 0; k < MI / 4; ++k) dst[k] = make_uint4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int mi = 0; mi < MI; ++mi) {
+        const float y[4] = {scaled(v[mi][0], w[0]), scaled(v[mi][1], w[1]), scaled(v[mi][2], w[0]),
+                            scaled(v[mi][3], w[1])};
+        write_frag(y, mi, n, b, h, rt, n_rows);
+      }
+    }
+  };
+
+  ArCursor nx = seg;  // the next tile this warp will ask for
+  int n_blk = -1, n_off = 0;
+  bool n_in = false;
+  auto issue = [&](int stage) {
+    copy(stage, nx, n_blk, n_off, n_in);
+    if (nx.i < count) advance(nx, 1);
+    look_up(nx, n_blk, n_off, n_in);
+  };
+  // The first tiles, after the first unit's query rows (which the copies would
+  // delay); the first two tiles' pages are asked for together.
+  auto start_copies = [&]() {
+    const ArCursor first = nx;
+    int f_blk, f_off = 0;
+    bool f_in;
+    look_up(first, f_blk, f_off, f_in);
+    if (nx.i < count) advance(nx, 1);
+    look_up(nx, n_blk, n_off, n_in);
+    copy(0, first, f_blk, f_off, f_in);
+#pragma unroll
+    for (int s = 1; s < S; ++s) issue(s);
+  };
 
   int stage = 0;
   while (seg.i < count) {
@@ -507,22 +567,28 @@ __global__ void __launch_bounds__(AR_THREADS, 1) attn_rows_kernel(const ArArgs p
     const long long p0 = (long long)__ldg(a.seq_len + seg.b) + a.t0;
     const int n_rows = min(p.RT, rows_of(seg.b) * p.G - seg.rt * p.RT);
     const long long plast = p0 + rows_of(seg.b) - 1;
-    load_q(seg, n_rows);
+    {
+      uint2 qv[C::ROWS];
+      fetch_q(seg, qv);
+      if (seg.i == 0) start_copies();
+      store_q(qv);
+    }
     // The rows' steps within the pass, as bytes past the first row's.
-    const int step0 = seg.rt * p.RT / p.G;
+    const int step0 = per_head(seg.rt * p.RT);
     uint32_t steps[(2 * NR + 3) / 4];
 #pragma unroll
     for (int i = 0; i < 2 * NR; ++i) {
-      const uint32_t d = (uint32_t)((seg.rt * p.RT + 8 * (i >> 1) + 2 * c + (i & 1)) / p.G - step0) << (8 * (i & 3));
+      const uint32_t d = (uint32_t)(per_head(seg.rt * p.RT + 8 * (i >> 1) + 2 * c + (i & 1)) - step0) << (8 * (i & 3));
       steps[i >> 2] = (i & 3) ? steps[i >> 2] | d : d;
     }
     auto step_of = [&](int n, int e) { return step0 + (int)((steps[(2 * n + e) >> 2] >> (8 * ((2 * n + e) & 3))) & 0xFFu); };
     float o[MI][NR][4], m[NR][2], l[NR][2], mul[NR][2];
+    uint32_t unset = (1u << (2 * NR)) - 1;  // rows that have no maximum yet
 #pragma unroll
     for (int n = 0; n < NR; ++n) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        m[n][e] = AR_EMPTY;
+        m[n][e] = 0.f;
         l[n][e] = 0.f;
         mul[n][e] = Q4 ? qmul[8 * n + 2 * c + e] : a.scale_log2;
       }
@@ -537,7 +603,7 @@ __global__ void __launch_bounds__(AR_THREADS, 1) attn_rows_kernel(const ArArgs p
       __syncwarp();
       const uint32_t st = ring + stage * C::STAGE_BYTES;
       const uint32_t there = vmask[warp * S + stage];
-      const int j0 = tile_start(seg.r, tile);
+      const int j0 = attn_tile_start<TILE>(seg.r, tile);
 
       // S^T = K Q^T
       float s[MT][NR][4];
@@ -577,23 +643,32 @@ __global__ void __launch_bounds__(AR_THREADS, 1) attn_rows_kernel(const ArArgs p
               lo[k] = hmul2(lo[k], sc[0][i >> 1]);
               hi[k] = hmul2(hi[k], sc[1][i >> 1]);
             }
+            uint4 q[NR];
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
+            for (int n = 0; n < NR; ++n) q[n] = lds_v4(qf + (i * NR + n) * 512);
 #pragma unroll
-              for (int n = 0; n < NR; ++n)
-                mma_16816<true>(s[t][n], lo[2 * k], hi[2 * k], lo[2 * k + 1], hi[2 * k + 1],
-                                lds_v2(qf + ((2 * i + k) * NR + n) * 256));
+            for (int n = 0; n < NR; ++n) mma_16816<true>(s[t][n], lo[0], hi[0], lo[1], hi[1], make_uint2(q[n].x, q[n].y));
+#pragma unroll
+            for (int n = 0; n < NR; ++n) mma_16816<true>(s[t][n], lo[2], hi[2], lo[3], hi[3], make_uint2(q[n].z, q[n].w));
           }
         }
       } else {
+        // Piece (2 ks + lane / 16) ^ (row & 7) of the row: the steps differ by
+        // an exclusive or of the (aligned) address.
         const int row = (lane & 7) + ((lane >> 3) & 1) * 8;
+        const uint32_t k0 = st + row * C::KROW + ((lane >> 4) ^ (row & 7)) * 16;
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-          uint32_t k4[4];
-          ldsm_x4(k4, st + row * C::KROW + (((2 * ks + (lane >> 4)) ^ (row & 7)) * 16));
+        for (int ks = 0; ks < KS; ks += 2) {
+          uint32_t ka[4], kb[4];
+          ldsm_x4(ka, k0 ^ (ks * 32));
+          ldsm_x4(kb, k0 ^ (ks * 32 + 32));
+          uint4 q[NR];
 #pragma unroll
-          for (int n = 0; n < NR; ++n)
-            mma_16816<false>(s[0][n], k4[0], k4[1], k4[2], k4[3], lds_v2(qf + (ks * NR + n) * 256));
+          for (int n = 0; n < NR; ++n) q[n] = lds_v4(qf + (ks / 2 * NR + n) * 512);
+#pragma unroll
+          for (int n = 0; n < NR; ++n) mma_16816<false>(s[0][n], ka[0], ka[1], ka[2], ka[3], make_uint2(q[n].x, q[n].y));
+#pragma unroll
+          for (int n = 0; n < NR; ++n) mma_16816<false>(s[0][n], kb[0], kb[1], kb[2], kb[3], make_uint2(q[n].z, q[n].w));
         }
       }
 
@@ -611,7 +686,7 @@ __global__ void __launch_bounds__(AR_THREADS, 1) attn_rows_kernel(const ArArgs p
 #pragma unroll
         for (int n = 0; n < NR; ++n)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) s[t][n][k] *= mul[n][k & 1];
+          for (int k = 0; k < 4; ++k) s[t][n][k] = fmaf(s[t][n][k], mul[n][k & 1], -m[n][k & 1]);
       if (edge) {
 #pragma unroll
         for (int n = 0; n < NR; ++n)
@@ -628,8 +703,9 @@ __global__ void __launch_bounds__(AR_THREADS, 1) attn_rows_kernel(const ArArgs p
           }
       }
 
-      // Move the maximum when some score lies far above it.
-      bool far = false;
+      // s is now relative to the running maximum (to 0 while a row has none);
+      // move that when some score lies far above it.
+      bool far = unset != 0;
       float mx[NR][2];
 #pragma unroll
       for (int n = 0; n < NR; ++n)
@@ -637,7 +713,7 @@ __global__ void __launch_bounds__(AR_THREADS, 1) attn_rows_kernel(const ArArgs p
         for (int e = 0; e < 2; ++e) {
           mx[n][e] = fmaxf(s[0][n][e], s[0][n][2 + e]);
           if (MT == 2) mx[n][e] = fmaxf(mx[n][e], fmaxf(s[MT - 1][n][e], s[MT - 1][n][2 + e]));
-          far |= mx[n][e] > m[n][e] + AR_SLACK;
+          far |= mx[n][e] > AR_SLACK;
         }
       if (__any_sync(0xffffffffu, far)) {
 #pragma unroll
@@ -645,13 +721,27 @@ __global__ void __launch_bounds__(AR_THREADS, 1) attn_rows_kernel(const ArArgs p
           float corr[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float v = mx[n][e];
+            float v = mx[n][e];  // how far the maximum moves
 #pragma unroll
             for (int x = 4; x < 32; x <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, x));
-            const float mn = fmaxf(m[n][e], v);
-            corr[e] = exp2_hw(m[n][e] - mn);
-            m[n][e] = mn;
+            const uint32_t bit = 1u << (2 * n + e);
+            corr[e] = 1.f;
+            if (unset & bit) {  // nothing to correct; a row that sees none of the tile stays without
+              if (v > -__builtin_huge_valf())
+                unset &= ~bit;
+              else
+                v = 0.f;
+            } else {
+              v = fmaxf(v, 0.f);
+              corr[e] = exp2_hw(-v);
+            }
+            m[n][e] += v;
             l[n][e] *= corr[e];
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
+              s[t][n][e] -= v;
+              s[t][n][2 + e] -= v;
+            }
           }
 #pragma unroll
           for (int i = 0; i < MI; ++i)
@@ -667,7 +757,7 @@ __global__ void __launch_bounds__(AR_THREADS, 1) attn_rows_kernel(const ArArgs p
         for (int n = 0; n < NR; ++n) {
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            s[t][n][k] = exp2_hw(s[t][n][k] - m[n][k & 1]);
+            s[t][n][k] = exp2_hw(s[t][n][k]);
             l[n][k & 1] += s[t][n][k];
           }
           pb[t][n].x = transpose_8x8(pack2<Q4>(s[t][n][0], s[t][n][1]));
@@ -769,10 +859,11 @@ __global__ void __launch_bounds__(AR_THREADS, 1) attn_rows_kernel(const ArArgs p
         }
       } else {
         const int row = (lane & 7) + (lane >> 4) * 8;
+        const uint32_t v0 = st + C::V_OFF + row * C::KROW + (((lane >> 3) & 1) ^ (row & 7)) * 16;
 #pragma unroll
         for (int mi = 0; mi < MI; ++mi) {
           uint32_t v4[4];
-          ldsm_x4_trans(v4, st + C::V_OFF + row * C::KROW + (((2 * mi + ((lane >> 3) & 1)) ^ (row & 7)) * 16));
+          ldsm_x4_trans(v4, v0 ^ (mi * 32));
 #pragma unroll
           for (int n = 0; n < NR; ++n) mma_16816<false>(o[mi][n], v4[0], v4[1], v4[2], v4[3], pb[0][n]);
         }
@@ -792,30 +883,12 @@ __global__ void __launch_bounds__(AR_THREADS, 1) attn_rows_kernel(const ArArgs p
     if (ta == 0 && end == seg.r.nt) {  // the whole unit: written
 #pragma unroll
       for (int n = 0; n < NR; ++n) {
-        const float w[2] = {weight(l[n][0]), weight(l[n][1])};
-        if (Q4) {
-          // A lane's elements of a row are D/8 in a run.
+        float v[MI][4];
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int lr = 8 * n + 2 * c + e;
-            uint32_t v[MI];
+        for (int mi = 0; mi < MI; ++mi)
 #pragma unroll
-            for (int mi = 0; mi < MI; ++mi)
-              v[mi] = pack2<false>(scaled(o[mi][n][e], w[e]), scaled(o[mi][n][2 + e], w[e]));
-            if (lr < n_rows) {
-              uint4 *dst = reinterpret_cast<uint4 *>(row_ptr(seg.b, seg.h, seg.rt, lr) + GD * g);
-#pragma unroll
-              for (int k = 0; k < MI / 4; ++k) dst[k] = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-            }
-          }
-        } else {
-#pragma unroll
-          for (int mi = 0; mi < MI; ++mi) {
-            const float v[4] = {scaled(o[mi][n][0], w[0]), scaled(o[mi][n][1], w[1]), scaled(o[mi][n][2], w[0]),
-                                scaled(o[mi][n][3], w[1])};
-            write_frag(v, mi, n, seg.b, seg.h, seg.rt, n_rows);
-          }
-        }
+          for (int k = 0; k < 4; ++k) v[mi][k] = o[mi][n][k];
+        write_rows(v, l[n], n, seg.b, seg.h, seg.rt, n_rows);
       }
     } else {  // a part of it: kept, in shared memory if it is the warp's last
       const bool last = seg.i + end - ta == count;
@@ -823,7 +896,7 @@ __global__ void __launch_bounds__(AR_THREADS, 1) attn_rows_kernel(const ArArgs p
       if (last) cp_async_wait<0>();  // (the groups left are empty; the ring's memory is free)
       __syncwarp();
       float4 *dst = last ? reinterpret_cast<float4 *>(smem + warp * C::RING)
-                         : reinterpret_cast<float4 *>(p.part + (size_t)(cta * AR_WARPS + warp) * AR_SLOT<D> + 64);
+                         : reinterpret_cast<float4 *>(p.part + (size_t)(cta * WARPS + warp) * AR_SLOT<D> + 64);
 #pragma unroll
       for (int mi = 0; mi < MI; ++mi)
 #pragma unroll
@@ -834,7 +907,7 @@ __global__ void __launch_bounds__(AR_THREADS, 1) attn_rows_kernel(const ArArgs p
         for (int n = 0; n < NR; ++n)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            sm_m[pc * C::ROWS + 8 * n + 2 * c + e] = m[n][e];
+            sm_m[pc * C::ROWS + 8 * n + 2 * c + e] = (unset >> (2 * n + e)) & 1u ? AR_EMPTY : m[n][e];
             sm_l[pc * C::ROWS + 8 * n + 2 * c + e] = l[n][e];
           }
       }
@@ -842,119 +915,171 @@ __global__ void __launch_bounds__(AR_THREADS, 1) attn_rows_kernel(const ArArgs p
     }
     advance(seg, end - ta);
   }
+  unseen();
   cp_async_wait<0>();
   __threadfence_block();
   __syncthreads();
 
   // --- join the parts of the units that cuts went through -------------------
-  float *cta_part = p.part + (size_t)gridDim.x * AR_WARPS * AR_SLOT<D>;
-  const long long c0 = sh.bound[0], c1 = sh.bound[AR_WARPS];
-  for (int i = 0; i < 2 * AR_WARPS;) {
-    const ArPiece u = sh.piece[i];
-    int j = i + 1;
-    if (u.g0 < 0) {
-      i = j;
-      continue;
+  float *cta_part = p.part + (size_t)gridDim.x * WARPS * AR_SLOT<D>;
+  const long long c0 = sh.bound[0], c1 = sh.bound[WARPS];
+  uint32_t parts, firsts;  // pieces there are; those that are their unit's first here
+  {
+    const long long g0 = lane < 2 * WARPS ? sh.piece[lane].g0 : -1;
+    parts = __ballot_sync(0xffffffffu, g0 >= 0);
+    const uint32_t below = parts & ((1u << lane) - 1u);
+    const long long prev = __shfl_sync(0xffffffffu, g0, below ? 31 - __clz(below) : 0);
+    firsts = __ballot_sync(0xffffffffu, g0 >= 0 && (!below || prev != g0));
+  }
+  auto pieces_of = [&](int i) {  // the pieces of the unit whose first is i
+    const uint32_t later = firsts & ~((2u << i) - 1u);
+    return parts & ~((1u << i) - 1u) & (later ? (later & (0u - later)) - 1u : 0xffffffffu);
+  };
+  // Every piece's weight and the unit's maximum and sum, a row per lane.
+  {
+    int turn = 0;
+    for (uint32_t left = firsts; left; left &= left - 1, ++turn) {
+      if (turn % WARPS != warp || lane >= C::ROWS) continue;
+      const int i = __ffs(left) - 1;
+      const uint32_t mine = pieces_of(i);
+      float m = AR_EMPTY, l = 0.f;
+      for (uint32_t k = mine; k; k &= k - 1) m = fmaxf(m, sm_m[(__ffs(k) - 1) * C::ROWS + lane]);
+      for (uint32_t k = mine; k; k &= k - 1) {
+        const int at = (__ffs(k) - 1) * C::ROWS + lane;
+        const float w = exp2_hw(sm_m[at] - m);
+        l += sm_l[at] * w;
+        sm_m[at] = w;
+      }
+      sm_l[i * C::ROWS + lane] = l;
+      sm_x[i * C::ROWS + lane] = m;
     }
-    while (j < 2 * AR_WARPS && (sh.piece[j].g0 == u.g0 || sh.piece[j].g0 < 0)) ++j;
-    const int n_rows = min(p.RT, rows_of(u.b) * p.G - u.rt * p.RT);
-    const bool here = u.g0 >= c0 && u.g0 + u.nt <= c1;  // no other CTA has tiles of it
-    float *slot = cta_part + (size_t)(2 * cta + (u.g0 >= c0)) * AR_SLOT<D>;
-    for (int f = warp; f < MI * NR; f += AR_WARPS) {
-      const int mi = f / NR, n = f - mi * NR;
+  }
+  __syncthreads();
+  // Items (unit, 8 rows, 32 elements of D) go to the warps in turn.
+  int shared0 = 0, shared1 = 0, n_shared = 0;  // units that other CTAs have tiles of: their first pieces
+  {
+    int item = warp;
+    for (uint32_t left = firsts; left; left &= left - 1) {
+      const int i = __ffs(left) - 1;
+      const uint32_t mine = pieces_of(i);
+      const ArPiece u = sh.piece[i];
+      const int n_rows = min(p.RT, rows_of(u.b) * p.G - u.rt * p.RT);
+      const bool here = u.g0 >= c0 && u.g0 + u.nt <= c1;
+      float *slot = cta_part + (size_t)(2 * cta + (u.g0 >= c0)) * AR_SLOT<D>;
+      if (!here) {
+        if (n_shared == 0)
+          shared0 = i;
+        else
+          shared1 = i;
+        ++n_shared;
+      }
+      for (; item < NR * MI / 2; item += WARPS) {
+        const int n = item % NR, mi = item / NR * 2, at = 8 * n + 2 * c;
+        float v[2][4];
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) v[x][k] = 0.f;
+#pragma unroll 2
+        for (uint32_t left_k = mine; left_k; left_k &= left_k - 1) {
+          const int k = __ffs(left_k) - 1;
+          const float4 *src = (k & 1) ? reinterpret_cast<const float4 *>(smem + (k >> 1) * C::RING)
+                                      : reinterpret_cast<const float4 *>(
+                                            p.part + (size_t)(cta * WARPS + (k >> 1)) * AR_SLOT<D> + 64);
+          const float2 w = *reinterpret_cast<const float2 *>(sm_m + k * C::ROWS + at);
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const float4 y = src[((mi + x) * NR + n) * 32 + lane];
+            v[x][0] += y.x * w.x;
+            v[x][1] += y.y * w.y;
+            v[x][2] += y.z * w.x;
+            v[x][3] += y.w * w.y;
+          }
+        }
+        const float2 l = *reinterpret_cast<const float2 *>(sm_l + i * C::ROWS + at);
+        if (here) {
+          const float w[2] = {weight(l.x), weight(l.y)};
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[x][k] = scaled(v[x][k], w[k & 1]);
+            write_frag(v[x], mi + x, n, u.b, u.h, u.rt, n_rows);
+          }
+        } else {
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+            reinterpret_cast<float4 *>(slot + 64)[((mi + x) * NR + n) * 32 + lane] =
+                make_float4(v[x][0], v[x][1], v[x][2], v[x][3]);
+          if (mi == 0 && g == 0) {
+            const float2 m = *reinterpret_cast<const float2 *>(sm_x + i * C::ROWS + at);
+            *reinterpret_cast<float4 *>(slot + 2 * at) = make_float4(m.x, l.x, m.y, l.y);
+          }
+        }
+      }
+      item -= NR * MI / 2;
+    }
+  }
+
+  // --- and of those that several CTAs share ---------------------------------
+  // At most two units: the one the CTA starts within and the one it ends within.
+  if (n_shared == 0) return;
+  __threadfence();  // this thread's sums, before the count
+  __syncthreads();
+  if (tid < n_shared) {
+    const ArPiece u = sh.piece[tid == 0 ? shared0 : shared1];
+    // CTAs ca .. cb hold tiles of the unit, ca its first.
+    auto cut = [&](int x) {
+      const long long raw = raw_cut(x * WARPS);
+      return raw > u.g0 && raw < u.g0 + u.nt ? u.g0 + snap((int)(raw - u.g0), u.nt) : raw;
+    };
+    int ca = cta, cb = cta;
+    while (cut(ca) > u.g0) --ca;
+    while (cb + 1 < P && cut(cb + 1) < u.g0 + u.nt) ++cb;
+    const bool last = atomicAdd(p.counters + ca, 1u) == (uint32_t)(cb - ca);
+    if (last) p.counters[ca] = 0;
+    sh.last[tid] = last;
+    sh.ca[tid] = ca;
+    sh.cb[tid] = cb;
+  }
+  __syncthreads();
+  for (int q = 0; q < n_shared; ++q) {
+    if (!sh.last[q]) continue;
+    __threadfence();
+    const ArPiece u = sh.piece[q == 0 ? shared0 : shared1];
+    const int n_rows = min(p.RT, rows_of(u.b) * p.G - u.rt * p.RT), ca = sh.ca[q], cb = sh.cb[q];
+    // slot 2 x + 1 of the CTA that holds the unit's first tile, 2 x of the others
+    auto of = [&](int x) { return cta_part + (size_t)(2 * x + (x == ca)) * AR_SLOT<D>; };
+    for (int f = warp; f < MI * NR; f += WARPS) {
+      const int mi = f / NR, n = f - mi * NR, at = 2 * (8 * n + 2 * c);
       float mj[2] = {AR_EMPTY, AR_EMPTY}, lj[2] = {0.f, 0.f}, v[4] = {0.f, 0.f, 0.f, 0.f};
-      for (int k = i; k < j; ++k)
-        if (sh.piece[k].g0 >= 0) {
-#pragma unroll
-          for (int e = 0; e < 2; ++e) mj[e] = fmaxf(mj[e], sm_m[k * C::ROWS + 8 * n + 2 * c + e]);
-        }
-      for (int k = i; k < j; ++k)
-        if (sh.piece[k].g0 >= 0) {
-          const float4 x =
-              (k & 1) ? reinterpret_cast<const float4 *>(smem + (k >> 1) * C::RING)[f * 32 + lane]
-                      : __ldcg(reinterpret_cast<const float4 *>(
-                                   p.part + (size_t)(cta * AR_WARPS + (k >> 1)) * AR_SLOT<D> + 64) + f * 32 + lane);
-          float w[2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            w[e] = exp2_hw(sm_m[k * C::ROWS + 8 * n + 2 * c + e] - mj[e]);
-            lj[e] += sm_l[k * C::ROWS + 8 * n + 2 * c + e] * w[e];
-          }
-          v[0] += x.x * w[0];
-          v[1] += x.y * w[1];
-          v[2] += x.z * w[0];
-          v[3] += x.w * w[1];
-        }
-      if (here) {
-        const float w[2] = {weight(lj[0]), weight(lj[1])};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = scaled(v[k], w[k & 1]);
-        write_frag(v, mi, n, u.b, u.h, u.rt, n_rows);
-      } else {
-        reinterpret_cast<float4 *>(slot + 64)[f * 32 + lane] = make_float4(v[0], v[1], v[2], v[3]);
-        if (mi == 0 && g == 0) {
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-            *reinterpret_cast<float2 *>(slot + 2 * (8 * n + 2 * c + e)) = make_float2(mj[e], lj[e]);
-        }
+#pragma unroll 8
+      for (int x = ca; x <= cb; ++x) {
+        const float4 ml = __ldcg(reinterpret_cast<const float4 *>(of(x) + at));
+        mj[0] = fmaxf(mj[0], ml.x);
+        mj[1] = fmaxf(mj[1], ml.z);
       }
-    }
-    if (!here) {
-      // CTAs ca .. cb hold tiles of the unit; ca holds its first.
-      auto cut = [&](int x) {
-        const long long raw = total * ((long long)x * AR_WARPS) / NW;
-        return raw > u.g0 && raw < u.g0 + u.nt ? u.g0 + snap((int)(raw - u.g0), u.nt) : raw;
-      };
-      int ca = cta, cb = cta;
-      while (cut(ca) > u.g0) --ca;
-      while (cb + 1 < P && cut(cb + 1) < u.g0 + u.nt) ++cb;
-      __threadfence();  // this thread's sums, before the count
-      __syncthreads();
-      if (tid == 0) {
-        const bool last = atomicAdd(p.counters + ca, 1u) == (uint32_t)(cb - ca);
-        if (last) p.counters[ca] = 0;
-        sh.last = last;
-      }
-      __syncthreads();
-      if (sh.last) {
-        __threadfence();
-        // slot 2 x + 1 of the CTA that holds the unit's first tile, 2 x of the others
-        auto of = [&](int x) { return cta_part + (size_t)(2 * x + (x == ca)) * AR_SLOT<D>; };
-        for (int f = warp; f < MI * NR; f += AR_WARPS) {
-          const int mi = f / NR, n = f - mi * NR, at = 2 * (8 * n + 2 * c);
-          float mj[2] = {AR_EMPTY, AR_EMPTY}, lj[2] = {0.f, 0.f}, v[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
-          for (int x = ca; x <= cb; ++x) {
-            const float4 ml = __ldcg(reinterpret_cast<const float4 *>(of(x) + at));
-            mj[0] = fmaxf(mj[0], ml.x);
-            mj[1] = fmaxf(mj[1], ml.z);
-          }
-#pragma unroll 4
-          for (int x = ca; x <= cb; ++x) {
-            const float4 ml = __ldcg(reinterpret_cast<const float4 *>(of(x) + at));
-            const float4 y = __ldcg(reinterpret_cast<const float4 *>(of(x) + 64) + f * 32 + lane);
-            const float w0 = exp2_hw(ml.x - mj[0]), w1 = exp2_hw(ml.z - mj[1]);
-            lj[0] += ml.y * w0;
-            lj[1] += ml.w * w1;
-            v[0] += y.x * w0;
-            v[1] += y.y * w1;
-            v[2] += y.z * w0;
-            v[3] += y.w * w1;
-          }
-          const float w[2] = {weight(lj[0]), weight(lj[1])};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) v[k] = scaled(v[k], w[k & 1]);
-          write_frag(v, mi, n, u.b, u.h, u.rt, n_rows);
-        }
+      for (int x = ca; x <= cb; ++x) {
+        const float4 ml = __ldcg(reinterpret_cast<const float4 *>(of(x) + at));
+        const float4 y = __ldcg(reinterpret_cast<const float4 *>(of(x) + 64) + f * 32 + lane);
+        const float w0 = exp2_hw(ml.x - mj[0]), w1 = exp2_hw(ml.z - mj[1]);
+        lj[0] += ml.y * w0;
+        lj[1] += ml.w * w1;
+        v[0] += y.x * w0;
+        v[1] += y.y * w1;
+        v[2] += y.z * w0;
+        v[3] += y.w * w1;
       }
-      __syncthreads();  // sh.last is written again
+      const float w[2] = {weight(lj[0]), weight(lj[1])};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = scaled(v[k], w[k & 1]);
+      write_frag(v, mi, n, u.b, u.h, u.rt, n_rows);
     }
-    i = j;
   }
 }
 
 size_t attn_rows_scratch_bytes(int D, int num_sms) {
-  return (size_t)(AR_WARPS + 2) * num_sms * (64 + 32 * (size_t)D) * 4;
+  return (size_t)(AR_MAX_WARPS + 2) * num_sms * (64 + 32 * (size_t)D) * 4;
 }
 
 template <bool Q4, int D, int NR>
@@ -969,7 +1094,7 @@ static cudaError_t launch_rows(const ArArgs &p, int num_sms, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     if (dev < 64) done[dev] = 1;
   }
-  return launch_pdl(attn_rows_kernel<Q4, D, NR>, dim3((unsigned)num_sms), dim3(AR_THREADS), smem, s, p);
+  return launch_pdl(attn_rows_kernel<Q4, D, NR>, dim3((unsigned)num_sms), dim3(ArCfg<Q4, D, NR>::THREADS), smem, s, p);
 }
 
 template <bool Q4, int D>
@@ -986,6 +1111,7 @@ cudaError_t launch_attn_rows(const AttnArgs &a, bool q4, float *part, uint32_t *
   ArArgs p;
   p.a = a;
   p.G = a.Hq / a.H;
+  p.G_magic = (uint32_t)(((1ull << 32) + p.G - 1) / p.G);
   const long long rq = (long long)a.rows_per_req * p.G;
   p.n_rt = (int)((rq + 31) / 32);
   p.RT = (int)((rq + p.n_rt - 1) / p.n_rt);

@@ -225,6 +225,8 @@ cudaError_t launch_attn_general(const AttnArgs &a, bool q4, cudaStream_t s);
 // (attn_rows.cu): attn_rows_scratch_bytes of partial sums and one counter per
 // SM (zero between calls).
 size_t attn_rows_scratch_bytes(int D, int num_sms);
+// Many rows a request, the same heads (attn_prompt.cu): no scratch.
+cudaError_t launch_attn_prompt(const AttnArgs &a, bool q4, cudaStream_t s);
 cudaError_t launch_attn_rows(const AttnArgs &a, bool q4, float *part, uint32_t *counters, int num_sms, cudaStream_t s);
 
 }  // namespace mlora
