@@ -37,4 +37,13 @@ __device__ __forceinline__ int div_heads(int r, int G, uint32_t magic) {
   return G == 1 ? r : (int)__umulhi((uint32_t)r, magic);
 }
 
+// 2^y by the hardware's approximation, results below 2^-126 as 0: a weight that
+// small is nothing beside the sum, which holds a 1 or more.  (The probabilities
+// of prob.cuh keep subnormals, at four times the instructions.)
+__device__ __forceinline__ float exp2_weight(float y) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(y));
+  return r;
+}
+
 }  // namespace mlora

@@ -20,7 +20,6 @@
 // the 4-bit cache they expand codes to fp16 on the way, exactly.
 #include "attn_common.cuh"
 #include "e2m1.cuh"
-#include "prob.cuh"
 
 namespace mlora {
 
@@ -78,6 +77,23 @@ __device__ __forceinline__ void tmem_ld_wait32(uint32_t (&r)[32]) {
                  "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
                :
                : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld_wait16(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+          taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
 }
 
 __device__ __forceinline__ void tmem_st_x32(uint32_t taddr, const uint32_t *r) {
@@ -280,59 +296,75 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prompt_kernel(const ApArgs
           const int jp = j0 + jj;
           return ((bits >> (jj & 31)) & 1u) && jp <= hi && (jp > lo || jp < a.sinks);
         };
-        uint32_t P[64];
-        float sum = 0.f;
-        // At most two more passes: past 2^27 a score's rounding exceeds the slack.
-        for (int pass = 0; pass < 3; ++pass) {
+        // Scores 32 at a time; the next are on their way meanwhile.  P goes over
+        // scores that have been read.
+        uint32_t s[2][32];
+        tmem_ld_x32(ts, s[0]);
+#pragma unroll
+        for (int ch = 0; ch < 4; ++ch) {
+          uint32_t(&x)[32] = s[ch & 1];
+          tmem_ld_wait32(x);
+          if (ch < 3) tmem_ld_x32(ts + 32 * (ch + 1), s[(ch + 1) & 1]);
+          float v[32];
           const float base = m == AP_NONE ? 0.f : m;
           float mx = AP_NONE;
-          sum = 0.f;
 #pragma unroll
-          for (int ch = 0; ch < 4; ++ch) {
-            uint32_t x[32];
-            tmem_ld_x32(ts + 32 * ch, x);
-            tmem_ld_wait32(x);
-            float v[32];
+          for (int i = 0; i < 32; ++i) v[i] = fmaf(__uint_as_float(x[i]), mul, -base);
+          if (edge) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = fmaf(__uint_as_float(x[i]), mul, -base);
-            if (edge) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (!sees(32 * ch + i, there[ch])) v[i] = AP_NONE;
-            }
-#pragma unroll
-            for (int i = 0; i < 32; ++i) mx = fmaxf(mx, v[i]);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = exp2_hw(v[i]);
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              sum += v[i] + v[i + 1];
-              P[16 * ch + i / 2] = ap_pack2<Q4>(v[i], v[i + 1]);
-            }
+            for (int i = 0; i < 32; ++i)
+              if (!sees(32 * ch + i, there[ch])) v[i] = AP_NONE;
           }
+#pragma unroll
+          for (int i = 0; i < 32; ++i) mx = fmaxf(mx, v[i]);
           const bool far = mx > AP_SLACK || (m == AP_NONE && mx > AP_NONE);
-          if (pass == 2 || !__any_sync(0xffffffffu, far)) break;
-          // Move the maximum of the rows that need it, rescale what is summed so far, take the tile again.
-          float corr = 1.f;
-          if (far) {
-            if (m != AP_NONE) corr = exp2_hw(-mx);
-            m = base + mx;
+          if (__any_sync(0xffffffffu, far)) {
+            // The maximum of the rows that need it moves by a whole number, so
+            // that what is summed so far, this tile's P too, scales exactly.
+            const float by = far ? floorf(mx) : 0.f;
+            const float corr = far && m != AP_NONE ? exp2_weight(-by) : 1.f;
+            if (far) m = base + by;
             l *= corr;
-          }
-          if (j > 0) {
 #pragma unroll
-            for (int i = 0; i < D; i += 32) {
-              uint32_t o[32];
-              tmem_ld_x32(to + i, o);
-              tmem_ld_wait32(o);
+            for (int i = 0; i < 32; ++i) v[i] -= by;
+            if (j > 0) {
+              for (int i = 0; i < D; i += 16) {
+                uint32_t o[16];
+                tmem_ld_x16(to + i, o);
+                tmem_ld_wait16(o);
 #pragma unroll
-              for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * corr);
-              tmem_st_x32(to + i, o);
+                for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * corr);
+                tmem_st_x16(to + i, o);
+              }
             }
-            tmem_st_wait();
+            if (!odd) {
+              tmem_st_wait();
+              for (int i = 0; i < 16 * ch; i += 16) {
+                uint32_t o[16];
+                tmem_ld_x16(ts + i, o);
+                tmem_ld_wait16(o);
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                  const float x0 = Q4 ? f16_lo(o[k]) : __uint_as_float(o[k] << 16);
+                  const float x1 = Q4 ? f16_hi(o[k]) : __uint_as_float(o[k] & 0xFFFF0000u);
+                  o[k] = ap_pack2<Q4>(x0 * corr, x1 * corr);
+                }
+                tmem_st_x16(ts + i, o);
+              }
+            }
           }
+          uint32_t pk[16];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = exp2_weight(v[i]);
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) pk[i / 2] = ap_pack2<Q4>(v[i], v[i + 1]);
+#pragma unroll
+          for (int n = 16; n > 0; n >>= 1)
+#pragma unroll
+            for (int i = 0; i < n; ++i) v[i] += v[i + n];
+          l += v[0];
+          if (!odd) tmem_st_x16(ts + 16 * ch, pk);
         }
-        l += sum;
         if (odd) {
           // Values that are not finite and that some rows do not see: the
           // product would bring 0 times them to those rows.  This tile is added
@@ -353,7 +385,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prompt_kernel(const ApArgs
               asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(s1) : : "memory");
               const uint32_t bits = jj < 64 ? (jj < 32 ? there[0] : there[1]) : (jj < 96 ? there[2] : there[3]);
               if (sees(jj, bits)) {
-                const float w = exp2_hw(fmaf(__uint_as_float(s1), mul, -base));
+                const float w = exp2_weight(fmaf(__uint_as_float(s1), mul, -base));
                 const uint8_t *v = smem + C::V_OFF + (j & 1) * C::OPERAND + (d0 >> 6) * C::BLOCK + jj * 128;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
@@ -372,9 +404,6 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prompt_kernel(const ApArgs
             }
             tmem_st_x32(to + d0, o);
           }
-        } else {
-          tmem_st_x32(ts, P);
-          tmem_st_x32(ts + 32, P + 32);
         }
         tmem_st_wait();
         tc_fence_before_sync();
@@ -476,9 +505,14 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prompt_kernel(const ApArgs
       const int j0 = attn_tile_start<AP_TILE>(R, j), jl = j0 + AP_TILE - 1;
       return jl > p_lo || (a.window && !(j0 > p_hi - a.window || jl < a.sinks));
     };
-    auto room = [&](int x) {  // the half-tile's place is free
+    auto room = [&](int x) {  // wait until the half-tile's place is free
       const int j = x >> 3;
       return j < 2 || __all_sync(0xffffffffu, wait(x & 4 ? &sh.v_empty[j & 1] : &sh.k_empty[j & 1], (j >> 1) - 1));
+    };
+    auto room_now = [&](int x) {
+      const int j = x >> 3;
+      return j < 2 ||
+             __all_sync(0xffffffffu, mbar_test(x & 4 ? &sh.v_empty[j & 1] : &sh.k_empty[j & 1], ((j >> 1) - 1) & 1));
     };
     auto arrive = [&](int x) {  // this warp's part of it is there
       fence_proxy_async_smem();
@@ -510,11 +544,17 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prompt_kernel(const ApArgs
         }
         arrive(x);
       };
-      int x = w;
-      for (; x < n_groups; x += AP_LOADERS) {
+      int done = w;  // the warp's first group that is not finished
+      bool ok = true;
+      for (int x = w; x < n_groups; x += AP_LOADERS) {
         const int j = x >> 3, slot = next;
         next = slot_of(x + AP_LOADERS);
-        if (!room(x)) break;
+        if (!room_now(x)) {  // what is on its way is handed over before a wait
+          ap_cp_async_wait<0>();
+          for (; done < x; done += AP_LOADERS) finish(done);
+          ok = room(x);
+          if (!ok) break;
+        }
         const uint32_t there = __ballot_sync(0xffffffffu, slot >= 0);
         if ((x & 4) && lane == 0) sh.there[j & 1][x & 3] = there;
         const uint8_t *src = static_cast<const uint8_t *>(x & 4 ? a.v : a.k) + (size_t)h * D * 2 + ch * 16;
@@ -526,20 +566,15 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prompt_kernel(const ApArgs
           ap_cp_async_16(dst + row * 128 + ((ch & 7) ^ (row & 7)) * 16, src + (size_t)(uint32_t)max(s, 0) * stride, s >= 0);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
-        if (x >= 2 * AP_LOADERS) {  // two groups of this warp stay in flight
+        if (done <= x - 2 * AP_LOADERS) {  // two groups of this warp stay in flight
           ap_cp_async_wait<2>();
-          finish(x - 2 * AP_LOADERS);
+          finish(done);
+          done += AP_LOADERS;
         }
-      }
-      if (x >= n_groups) {
-        if (x >= 2 * AP_LOADERS) {
-          ap_cp_async_wait<1>();
-          finish(x - 2 * AP_LOADERS);
-        }
-        ap_cp_async_wait<0>();
-        if (x >= AP_LOADERS) finish(x - AP_LOADERS);
       }
       ap_cp_async_wait<0>();
+      if (ok)
+        for (; done < n_groups; done += AP_LOADERS) finish(done);
     } else {
       // Four lanes (D = 128) or two (D = 64) to a position, 16 bytes of codes
       // (32 elements, two scales) each.

@@ -35,7 +35,6 @@
 // 8 bytes of V codes are contiguous.
 #include "attn_common.cuh"
 #include "e2m1.cuh"
-#include "prob.cuh"
 
 namespace mlora {
 
@@ -733,7 +732,7 @@ __global__ void __launch_bounds__(ArCfg<Q4, D, NR>::THREADS, 1) attn_rows_kernel
                 v = 0.f;
             } else {
               v = fmaxf(v, 0.f);
-              corr[e] = exp2_hw(-v);
+              corr[e] = exp2_weight(-v);
             }
             m[n][e] += v;
             l[n][e] *= corr[e];
@@ -757,7 +756,7 @@ __global__ void __launch_bounds__(ArCfg<Q4, D, NR>::THREADS, 1) attn_rows_kernel
         for (int n = 0; n < NR; ++n) {
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            s[t][n][k] = exp2_hw(s[t][n][k]);
+            s[t][n][k] = exp2_weight(s[t][n][k]);
             l[n][k & 1] += s[t][n][k];
           }
           pb[t][n].x = transpose_8x8(pack2<Q4>(s[t][n][0], s[t][n][1]));
@@ -946,7 +945,7 @@ __global__ void __launch_bounds__(ArCfg<Q4, D, NR>::THREADS, 1) attn_rows_kernel
       for (uint32_t k = mine; k; k &= k - 1) m = fmaxf(m, sm_m[(__ffs(k) - 1) * C::ROWS + lane]);
       for (uint32_t k = mine; k; k &= k - 1) {
         const int at = (__ffs(k) - 1) * C::ROWS + lane;
-        const float w = exp2_hw(sm_m[at] - m);
+        const float w = exp2_weight(sm_m[at] - m);
         l += sm_l[at] * w;
         sm_m[at] = w;
       }
@@ -1062,7 +1061,7 @@ __global__ void __launch_bounds__(ArCfg<Q4, D, NR>::THREADS, 1) attn_rows_kernel
       for (int x = ca; x <= cb; ++x) {
         const float4 ml = __ldcg(reinterpret_cast<const float4 *>(of(x) + at));
         const float4 y = __ldcg(reinterpret_cast<const float4 *>(of(x) + 64) + f * 32 + lane);
-        const float w0 = exp2_hw(ml.x - mj[0]), w1 = exp2_hw(ml.z - mj[1]);
+        const float w0 = exp2_weight(ml.x - mj[0]), w1 = exp2_weight(ml.z - mj[1]);
         lj[0] += ml.y * w0;
         lj[1] += ml.w * w1;
         v[0] += y.x * w0;
