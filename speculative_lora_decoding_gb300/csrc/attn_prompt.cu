@@ -119,6 +119,32 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uin
       : "memory");
 }
 
+// v = x * mul + add, two at a time.
+__device__ __forceinline__ void fma_x32(float (&v)[32], const uint32_t (&x)[32], float mul, float add) {
+  uint64_t m2, a2;
+  asm("mov.b64 %0, {%1, %1};" : "=l"(m2) : "f"(mul));
+  asm("mov.b64 %0, {%1, %1};" : "=l"(a2) : "f"(add));
+#pragma unroll
+  for (int i = 0; i < 32; i += 2) {
+    uint64_t y;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "r"(x[i]), "r"(x[i + 1]));
+    asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(y) : "l"(m2), "l"(a2));
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(v[i]), "=f"(v[i + 1]) : "l"(y));
+  }
+}
+__device__ __forceinline__ float sum_x32(const float (&v)[32]) {
+  uint64_t y[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) asm("mov.b64 %0, {%1, %2};" : "=l"(y[i]) : "f"(v[2 * i]), "f"(v[2 * i + 1]));
+#pragma unroll
+  for (int n = 8; n > 0; n >>= 1)
+#pragma unroll
+    for (int i = 0; i < n; ++i) asm("add.rn.f32x2 %0, %0, %1;" : "+l"(y[i]) : "l"(y[i + n]));
+  float a, b;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(y[0]));
+  return a + b;
+}
+
 // V's tile as the second product's B operand: 16 positions (K) by D elements
 // (N), N contiguous: rows of 64 elements (128 bytes, swizzled), 8 positions
 // 1024 bytes apart (stride offset), the next 64 elements a block further
@@ -274,6 +300,17 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prompt_kernel(const ApArgs
       const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
       const uint32_t ts = tmem + lanes + 128 * half, to = tmem + lanes + 256 + 128 * half;
       float m = AP_NONE, l = 0.f;
+      auto rescale_o = [&](float corr) {
+#pragma unroll 1
+        for (int i = 0; i < D; i += 16) {
+          uint32_t o[16];
+          tmem_ld_x16(to + i, o);
+          tmem_ld_wait16(o);
+#pragma unroll
+          for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * corr);
+          tmem_st_x16(to + i, o);
+        }
+      };
       bool ok = true;
       for (int j = 0; j < nt; ++j) {
         ok = wait(&sh.s_full[half], j) && wait(&sh.v_full[j & 1], j >> 1);
@@ -298,47 +335,35 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prompt_kernel(const ApArgs
         };
         // Scores 32 at a time; the next are on their way meanwhile.  P goes over
         // scores that have been read.
-        uint32_t s[2][32];
-        tmem_ld_x32(ts, s[0]);
-#pragma unroll
-        for (int ch = 0; ch < 4; ++ch) {
-          uint32_t(&x)[32] = s[ch & 1];
-          tmem_ld_wait32(x);
-          if (ch < 3) tmem_ld_x32(ts + 32 * (ch + 1), s[(ch + 1) & 1]);
-          float v[32];
+        auto chunk = [&](int ch, uint32_t (&x)[32]) {
+          float v[32], mx[4] = {AP_NONE, AP_NONE, AP_NONE, AP_NONE};
           const float base = m == AP_NONE ? 0.f : m;
-          float mx = AP_NONE;
-#pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = fmaf(__uint_as_float(x[i]), mul, -base);
+          fma_x32(v, x, mul, -base);
           if (edge) {
+            const uint32_t bits = sh.there[j & 1][ch];
 #pragma unroll
             for (int i = 0; i < 32; ++i)
-              if (!sees(32 * ch + i, there[ch])) v[i] = AP_NONE;
+              if (!sees(32 * ch + i, bits)) v[i] = AP_NONE;
           }
 #pragma unroll
-          for (int i = 0; i < 32; ++i) mx = fmaxf(mx, v[i]);
-          const bool far = mx > AP_SLACK || (m == AP_NONE && mx > AP_NONE);
+          for (int i = 0; i < 32; i += 8)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mx[k] = fmaxf(fmaxf(mx[k], v[i + k]), v[i + k + 4]);
+          mx[0] = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          const bool far = mx[0] > AP_SLACK || (m == AP_NONE && mx[0] > AP_NONE);
           if (__any_sync(0xffffffffu, far)) {
             // The maximum of the rows that need it moves by a whole number, so
             // that what is summed so far, this tile's P too, scales exactly.
-            const float by = far ? floorf(mx) : 0.f;
+            const float by = far ? floorf(mx[0]) : 0.f;
             const float corr = far && m != AP_NONE ? exp2_weight(-by) : 1.f;
             if (far) m = base + by;
             l *= corr;
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] -= by;
-            if (j > 0) {
-              for (int i = 0; i < D; i += 16) {
-                uint32_t o[16];
-                tmem_ld_x16(to + i, o);
-                tmem_ld_wait16(o);
-#pragma unroll
-                for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * corr);
-                tmem_st_x16(to + i, o);
-              }
-            }
+            if (j > 0) rescale_o(corr);
             if (!odd) {
               tmem_st_wait();
+#pragma unroll 1
               for (int i = 0; i < 16 * ch; i += 16) {
                 uint32_t o[16];
                 tmem_ld_x16(ts + i, o);
@@ -358,12 +383,19 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prompt_kernel(const ApArgs
           for (int i = 0; i < 32; ++i) v[i] = exp2_weight(v[i]);
 #pragma unroll
           for (int i = 0; i < 32; i += 2) pk[i / 2] = ap_pack2<Q4>(v[i], v[i + 1]);
-#pragma unroll
-          for (int n = 16; n > 0; n >>= 1)
-#pragma unroll
-            for (int i = 0; i < n; ++i) v[i] += v[i + n];
-          l += v[0];
+          l += sum_x32(v);
           if (!odd) tmem_st_x16(ts + 16 * ch, pk);
+        };
+        uint32_t s0[32], s1[32];
+        tmem_ld_x32(ts, s0);
+#pragma unroll 1
+        for (int ch = 0; ch < 4; ch += 2) {
+          tmem_ld_wait32(s0);
+          tmem_ld_x32(ts + 32 * ch + 32, s1);
+          chunk(ch, s0);
+          tmem_ld_wait32(s1);
+          if (ch == 0) tmem_ld_x32(ts + 64, s0);
+          chunk(ch + 1, s1);
         }
         if (odd) {
           // Values that are not finite and that some rows do not see: the
