@@ -15,9 +15,12 @@
 // then a tile is one pass over its scores.
 //
 // Warps 0-3 and 4-7 hold the rows of the two halves, warp 8 issues the MMAs,
-// warps 9-11 bring the tiles: a gather of 16-byte pieces through the block
-// table into 128-byte-swizzled rows (K read K-major, V along its rows); over
-// the 4-bit cache they expand codes to fp16 on the way, exactly.
+// warps 9-11 bring the tiles into 128-byte-swizzled rows (K read K-major, V
+// along its rows), in one of three ways:
+//   boxes   bf16 cache whose pages are multiples of 8 positions: warp 9 copies
+//           boxes of a page's positions by TMA, a lane to a box;
+//   pieces  other pages: all three gather 16-byte pieces;
+//   codes   4-bit cache: all three expand codes to fp16 on the way, exactly.
 #include "attn_common.cuh"
 #include "e2m1.cuh"
 
@@ -43,12 +46,14 @@ struct ApCfg {
   static constexpr int SMEM = BAR_OFF + 512 + 1024;     // and the alignment
 };
 
+enum { AP_BOXES = 0, AP_PIECES = 1, AP_CODES = 2 };
+
 struct ApShared {
-  uint64_t q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full[2], fin;
+  uint64_t q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], v_land[2], s_full[2], p_full[2], o_full[2], fin;
   uint32_t tmem;
   int abort;
-  uint32_t there[2][AP_GROUPS];  // per V stage: positions whose slot is in the cache
-  int odd[2][AP_GROUPS];         // per V stage: some V that not every row sees is not finite
+  uint32_t there[4][AP_GROUPS];  // of the last tiles: positions whose slot is in the cache
+  int odd[2][AP_GROUPS];         // per V stage, tiles that not every row sees whole: some V is not finite
 };
 static_assert(sizeof(ApShared) <= 512, "ApShared");
 
@@ -58,6 +63,7 @@ struct ApArgs {
   uint32_t G_magic;
   int extent, bs_shift;
   int n_rt, halves;  // row tiles per (request, cache head), of halves * 128 rows
+  int box;           // positions of a TMA box
 };
 
 __device__ __forceinline__ void ap_cp_async_16(uint32_t dst, const void *src, bool there) {
@@ -132,6 +138,21 @@ __device__ __forceinline__ void fma_x32(float (&v)[32], const uint32_t (&x)[32],
     asm("mov.b64 {%0, %1}, %2;" : "=f"(v[i]), "=f"(v[i + 1]) : "l"(y));
   }
 }
+// The largest of y and 32 values (NaN left out).
+__device__ __forceinline__ float max_x32(const uint32_t (&x)[32], float y) {
+  float m[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    m[k] = __uint_as_float(x[8 * k + 7]);
+#pragma unroll
+    for (int i = 0; i < 6; i += 2)
+      asm("max.f32 %0, %0, %1, %2;"
+          : "+f"(m[k])
+          : "f"(__uint_as_float(x[8 * k + i])), "f"(__uint_as_float(x[8 * k + i + 1])));
+    m[k] = fmaxf(m[k], __uint_as_float(x[8 * k + 6]));
+  }
+  return fmaxf(fmaxf(m[0], m[1]), fmaxf(fmaxf(m[2], m[3]), y));
+}
 __device__ __forceinline__ float sum_x32(const float (&v)[32]) {
   uint64_t y[16];
 #pragma unroll
@@ -180,9 +201,11 @@ __device__ __forceinline__ uint32_t ap_hmul2(uint32_t a, uint32_t b) {
   return r;
 }
 
-template <bool Q4, int D>
-__global__ void __launch_bounds__(AP_THREADS, 1) attn_prompt_kernel(const ApArgs p) {
+template <int MODE, int D>
+__global__ void __launch_bounds__(AP_THREADS, 1)
+    attn_prompt_kernel(const ApArgs p, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
   using C = ApCfg<D>;
+  constexpr bool Q4 = MODE == AP_CODES;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = align_smem_1024(smem_raw);
   ApShared &sh = *reinterpret_cast<ApShared *>(smem + C::BAR_OFF);
@@ -220,8 +243,9 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prompt_kernel(const ApArgs
     mbar_init(&sh.q_full, 128 * halves);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&sh.k_full[i], AP_GROUPS);
-      mbar_init(&sh.v_full[i], AP_GROUPS);
+      mbar_init(&sh.k_full[i], MODE == AP_BOXES ? 1 : AP_GROUPS);
+      mbar_init(&sh.v_full[i], MODE == AP_BOXES ? 1 : AP_GROUPS);
+      mbar_init(&sh.v_land[i], 1);
       mbar_init(&sh.k_empty[i], 1);
       mbar_init(&sh.v_empty[i], 1);
       mbar_init(&sh.s_full[i], 1);
@@ -244,11 +268,22 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prompt_kernel(const ApArgs
   const uint32_t tmem = sh.tmem;
   volatile int *abort = &sh.abort;
   auto wait = [&](uint64_t *bar, uint32_t parity) {
+    if (*abort) return false;
     if (mbar_wait_bounded(bar, parity & 1u, abort)) return true;
     *abort = 1;
     return false;
   };
   // S (and P over it) of half i at column 128 i, O at 256 + 128 i.
+
+  // Whether some row of the CTA does not see all of tile j.
+  auto partial = [&](int j) {
+    const int j0 = attn_tile_start<AP_TILE>(R, j), jl = j0 + AP_TILE - 1;
+    return jl > p_lo || (a.window && !(j0 > p_hi - a.window || jl < a.sinks));
+  };
+  auto is_odd = [&](int j) {  // (V of tile j has landed)
+    const int *f = sh.odd[j & 1];
+    return MODE == AP_BOXES ? f[0] != 0 : (f[0] | f[1] | f[2] | f[3]) != 0;
+  };
 
   if (warp < 8) {
     const int half = warp >> 2;
@@ -261,7 +296,8 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prompt_kernel(const ApArgs
       const int hi = (int)min(pos, 0x7fffffffll);  // sees j <= hi, j > lo or j < sinks
       const int lo = a.window ? (int)max(min(pos - a.window, 0x7fffffffll), -1ll) : -1;
       const int hi_first = __shfl_sync(0xffffffffu, hi, 0), lo_last = __shfl_sync(0xffffffffu, lo, 31);
-      float mul = a.scale_log2;
+      float mul = fabsf(a.scale_log2);  // (a negative scale's sign goes into q)
+      const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;
       {
         const uint16_t *src = a.y + (size_t)(b * T + t) * a.ld + a.q_col + (size_t)(h * p.G + rc - t * p.G) * D;
         uint8_t *dst = smem + C::Q_OFF + half * C::OPERAND + row * 128;
@@ -284,6 +320,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prompt_kernel(const ApArgs
 #pragma unroll
         for (int i = 0; i < D / 8; ++i) {
           uint4 v = valid ? __ldg(reinterpret_cast<const uint4 *>(src) + i) : make_uint4(0, 0, 0, 0);
+          v = make_uint4(v.x ^ flip, v.y ^ flip, v.z ^ flip, v.w ^ flip);
           if (Q4) {
             uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -313,95 +350,87 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prompt_kernel(const ApArgs
       };
       bool ok = true;
       for (int j = 0; j < nt; ++j) {
-        ok = wait(&sh.s_full[half], j) && wait(&sh.v_full[j & 1], j >> 1);
+        const bool part = partial(j);
+        ok = wait(&sh.s_full[half], j) && (!part || wait(&sh.v_full[j & 1], j >> 1));
         if (!__all_sync(0xffffffffu, ok)) {
           ok = false;
           break;
         }
         tc_fence_after_sync();
         const int j0 = attn_tile_start<AP_TILE>(R, j), jl = j0 + AP_TILE - 1;
-        uint32_t there[4];
-        int odd = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          there[i] = sh.there[j & 1][i];
-          odd |= sh.odd[j & 1][i];
-        }
+        const uint32_t *there = sh.there[j & 3];
+        const bool odd = part && is_odd(j);
         const bool edge = (there[0] & there[1] & there[2] & there[3]) != 0xffffffffu || jl > hi_first ||
                           (a.window && !(j0 > lo_last || jl < a.sinks));
         auto sees = [&](int jj, uint32_t bits) {
           const int jp = j0 + jj;
           return ((bits >> (jj & 31)) & 1u) && jp <= hi && (jp > lo || jp < a.sinks);
         };
-        // Scores 32 at a time; the next are on their way meanwhile.  P goes over
-        // scores that have been read.
-        auto chunk = [&](int ch, uint32_t (&x)[32]) {
-          float v[32], mx[4] = {AP_NONE, AP_NONE, AP_NONE, AP_NONE};
-          const float base = m == AP_NONE ? 0.f : m;
-          fma_x32(v, x, mul, -base);
-          if (edge) {
-            const uint32_t bits = sh.there[j & 1][ch];
+        // First the row's maximum, over all scores, 32 at a time while the next
+        // are on their way; then the weights, with no decision among them.  P
+        // goes over the first scores, which are the last to be looked at and
+        // still in registers then.
+        uint32_t s0[32], s1[32];
+        auto hide = [&](uint32_t (&x)[32], int ch) {
+          const uint32_t bits = there[ch];
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (!sees(32 * ch + i, bits)) v[i] = AP_NONE;
-          }
-#pragma unroll
-          for (int i = 0; i < 32; i += 8)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) mx[k] = fmaxf(fmaxf(mx[k], v[i + k]), v[i + k + 4]);
-          mx[0] = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-          const bool far = mx[0] > AP_SLACK || (m == AP_NONE && mx[0] > AP_NONE);
-          if (__any_sync(0xffffffffu, far)) {
-            // The maximum of the rows that need it moves by a whole number, so
-            // that what is summed so far, this tile's P too, scales exactly.
-            const float by = far ? floorf(mx[0]) : 0.f;
-            const float corr = far && m != AP_NONE ? exp2_weight(-by) : 1.f;
-            if (far) m = base + by;
-            l *= corr;
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] -= by;
-            if (j > 0) rescale_o(corr);
-            if (!odd) {
-              tmem_st_wait();
-#pragma unroll 1
-              for (int i = 0; i < 16 * ch; i += 16) {
-                uint32_t o[16];
-                tmem_ld_x16(ts + i, o);
-                tmem_ld_wait16(o);
-#pragma unroll
-                for (int k = 0; k < 16; ++k) {
-                  const float x0 = Q4 ? f16_lo(o[k]) : __uint_as_float(o[k] << 16);
-                  const float x1 = Q4 ? f16_hi(o[k]) : __uint_as_float(o[k] & 0xFFFF0000u);
-                  o[k] = ap_pack2<Q4>(x0 * corr, x1 * corr);
-                }
-                tmem_st_x16(ts + i, o);
-              }
-            }
-          }
+          for (int i = 0; i < 32; ++i)
+            if (!sees(32 * ch + i, bits)) x[i] = 0xff800000u;  // -infinity
+        };
+        tmem_ld_x32(ts + 64, s0);
+        tmem_ld_wait32(s0);
+        tmem_ld_x32(ts + 96, s1);
+        if (edge) hide(s0, 2);
+        float mx = max_x32(s0, AP_NONE);
+        tmem_ld_wait32(s1);
+        tmem_ld_x32(ts, s0);
+        if (edge) hide(s1, 3);
+        mx = max_x32(s1, mx);
+        tmem_ld_wait32(s0);
+        tmem_ld_x32(ts + 32, s1);
+        if (edge) hide(s0, 0);
+        mx = max_x32(s0, mx);
+        tmem_ld_wait32(s1);
+        if (edge) hide(s1, 1);
+        mx = max_x32(s1, mx);
+        float base = m == AP_NONE ? 0.f : m;
+        const float d = fmaf(mx, mul, -base);
+        const bool far = mx > AP_NONE && (d > AP_SLACK || m == AP_NONE);
+        if (__any_sync(0xffffffffu, far)) {
+          // The maximum of the rows that need it moves by a whole number, so
+          // that what is summed so far scales exactly.
+          const float by = far ? floorf(d) : 0.f;
+          const float corr = far && m != AP_NONE ? exp2_weight(-by) : 1.f;
+          if (far) m = base = base + by;
+          l *= corr;
+          if (j > 0) rescale_o(corr);
+        }
+        auto weights = [&](uint32_t (&x)[32], int ch) {
+          float v[32];
           uint32_t pk[16];
+          fma_x32(v, x, mul, -base);
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] = exp2_weight(v[i]);
 #pragma unroll
           for (int i = 0; i < 32; i += 2) pk[i / 2] = ap_pack2<Q4>(v[i], v[i + 1]);
-          l += sum_x32(v);
           if (!odd) tmem_st_x16(ts + 16 * ch, pk);
+          return sum_x32(v);
         };
-        uint32_t s0[32], s1[32];
-        tmem_ld_x32(ts, s0);
-#pragma unroll 1
-        for (int ch = 0; ch < 4; ch += 2) {
-          tmem_ld_wait32(s0);
-          tmem_ld_x32(ts + 32 * ch + 32, s1);
-          chunk(ch, s0);
-          tmem_ld_wait32(s1);
-          if (ch == 0) tmem_ld_x32(ts + 64, s0);
-          chunk(ch + 1, s1);
-        }
+        float sum = weights(s0, 0);
+        tmem_ld_x32(ts + 64, s0);
+        sum += weights(s1, 1);
+        tmem_ld_wait32(s0);
+        tmem_ld_x32(ts + 96, s1);
+        if (edge) hide(s0, 2);
+        sum += weights(s0, 2);
+        tmem_ld_wait32(s1);
+        if (edge) hide(s1, 3);
+        sum += weights(s1, 3);
+        l += sum;
         if (odd) {
           // Values that are not finite and that some rows do not see: the
           // product would bring 0 times them to those rows.  This tile is added
           // up here, a position at a time (the MMA warp leaves it out).
-          const float base = m == AP_NONE ? 0.f : m;
           for (int d0 = 0; d0 < D; d0 += 32) {
             uint32_t o[32];
             if (j > 0) {
@@ -415,8 +444,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prompt_kernel(const ApArgs
               uint32_t s1;
               tmem_ld_x1(ts + jj, s1);
               asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(s1) : : "memory");
-              const uint32_t bits = jj < 64 ? (jj < 32 ? there[0] : there[1]) : (jj < 96 ? there[2] : there[3]);
-              if (sees(jj, bits)) {
+              if (sees(jj, there[jj >> 5])) {
                 const float w = exp2_weight(fmaf(__uint_as_float(s1), mul, -base));
                 const uint8_t *v = smem + C::V_OFF + (j & 1) * C::OPERAND + (d0 >> 6) * C::BLOCK + jj * 128;
 #pragma unroll
@@ -468,14 +496,18 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prompt_kernel(const ApArgs
     }
   } else if (warp == AP_MMA_WARP) {
     // --- the MMAs, issued by lane 0 -------------------------------------------
-    const uint32_t q0 = smem_addr(smem + C::Q_OFF), k0 = smem_addr(smem + C::K_OFF), v0 = smem_addr(smem + C::V_OFF);
+    const uint64_t q0 = smem_desc_kmajor_sw128(smem_addr(smem + C::Q_OFF)),
+                   k0 = smem_desc_kmajor_sw128(smem_addr(smem + C::K_OFF)),
+                   v0 = smem_desc_nmajor_sw128(smem_addr(smem + C::V_OFF), C::BLOCK);
     constexpr uint32_t ID_S = ap_idesc<Q4>(AP_TILE, false), ID_O = ap_idesc<Q4>(D, true);
+    constexpr uint32_t STEP = C::OPERAND >> 4;  // in a descriptor's address units
     auto scores = [&](int j, int half) {
+      const uint64_t q = q0 + half * STEP, k = k0 + (j & 1) * STEP;
 #pragma unroll
       for (int ks = 0; ks < D / 16; ++ks) {
-        const uint32_t off = (ks >> 2) * C::BLOCK + (ks & 3) * 32;
-        mma_bf16_ss(tmem + 128 * half, smem_desc_kmajor_sw128(q0 + half * C::OPERAND + off),
-                    smem_desc_kmajor_sw128(k0 + (j & 1) * C::OPERAND + off), ID_S, ks > 0);
+        constexpr uint32_t B16 = C::BLOCK >> 4;
+        const uint32_t off = (ks >> 2) * B16 + (ks & 3) * 2;
+        mma_bf16_ss(tmem + 128 * half, q + off, k + off, ID_S, ks > 0);
       }
       mma_commit(&sh.s_full[half]);
       if (half == halves - 1) mma_commit(&sh.k_empty[j & 1]);
@@ -494,12 +526,11 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prompt_kernel(const ApArgs
         if (!ok) break;
         tc_fence_after_sync();
         if (lane == 0) {
-          const bool odd = sh.odd[j & 1][0] | sh.odd[j & 1][1] | sh.odd[j & 1][2] | sh.odd[j & 1][3];
-          if (!odd) {
+          if (!(partial(j) && is_odd(j))) {
+            const uint64_t v = v0 + (j & 1) * STEP;
 #pragma unroll
             for (int kk = 0; kk < AP_TILE / 16; ++kk)
-              mma_f16_ts(tmem + 256 + 128 * half, tmem + 128 * half + 8 * kk,
-                         smem_desc_nmajor_sw128(v0 + (j & 1) * C::OPERAND + kk * 2048, C::BLOCK), ID_O, j > 0 || kk > 0);
+              mma_f16_ts(tmem + 256 + 128 * half, tmem + 128 * half + 8 * kk, v + kk * 128, ID_O, j > 0 || kk > 0);
           }
           if (half == halves - 1) mma_commit(&sh.v_empty[j & 1]);
           if (j + 1 < nt)
@@ -514,6 +545,106 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prompt_kernel(const ApArgs
       int never = 0;
       if (lane == 0) mma_commit(&sh.fin);
       mbar_wait_bounded(&sh.fin, 0, &never);
+    }
+  } else if (MODE == AP_BOXES) {
+    if (warp == AP_MMA_WARP + 1) {
+      // --- the tiles, by TMA: lane i brings the tile's box i ---------------------
+      const int n_box = AP_TILE / p.box, bytes = p.box * 128 * (D / 64);
+      auto slot_of = [&](int j) {  // the box's first slot; -1: none
+        if (j >= nt || lane >= n_box) return -1;
+        const int pos = attn_tile_start<AP_TILE>(R, j) + lane * p.box;
+        if (pos >= (j < R.st ? R.sink : R.n)) return -1;
+        const int page = p.bs_shift >= 0 ? pos >> p.bs_shift : pos / a.block_size;
+        const int blk = __ldg(a.block_table + (size_t)b * a.max_blocks + page);
+        if (blk < 0 || blk >= a.num_blocks) {
+          raise_status(a.status, MLORA_DEV_BAD_SLOT);
+          return -1;
+        }
+        return blk * a.block_size + pos - page * a.block_size;
+      };
+      const uint64_t policy = policy_evict_last();  // other rows of the head read the tile again
+      int next = slot_of(0), lands[2] = {0, 0};
+      uint64_t *last_bar[2][2] = {};  // the last copies' barriers and parities
+      uint32_t last_parity[2][2] = {};
+      bool ok = true;
+      for (int j = 0; j < nt && ok; ++j) {
+        const int slot = next;
+        next = slot_of(j + 1);
+        const uint32_t there = __ballot_sync(0xffffffffu, slot >= 0);
+        const uint32_t all = n_box == 32 ? 0xffffffffu : (1u << n_box) - 1u;
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+          ok = j < 2 || __all_sync(0xffffffffu, wait(v ? &sh.v_empty[j & 1] : &sh.k_empty[j & 1], (j >> 1) - 1));
+          if (!ok) break;
+          uint8_t *dst = smem + (v ? C::V_OFF : C::K_OFF) + (j & 1) * C::OPERAND;
+          if (there != all) {  // boxes that are not read are zeros
+            for (uint32_t left = all & ~there; left; left &= left - 1) {
+              const int i = __ffs(left) - 1;
+              for (int e = lane; e < p.box * 8 * (D / 64); e += 32) {
+                const int blk = e / (p.box * 8), at = e - blk * p.box * 8;
+                *reinterpret_cast<uint4 *>(dst + blk * C::BLOCK + i * p.box * 128 + at * 16) = make_uint4(0, 0, 0, 0);
+              }
+            }
+            fence_proxy_async_smem();
+          }
+          if (!v && lane < AP_GROUPS) {
+            uint32_t bits = 0xffffffffu;
+            if (there != all) {
+              bits = 0;
+              for (int i = 0; i < 32; ++i) bits |= ((there >> ((32 * lane + i) / p.box)) & 1u) << i;
+            }
+            sh.there[j & 3][lane] = bits;
+          }
+          __syncwarp();
+          // A tile with values that some row does not see is looked over first.
+          const bool land = v && partial(j);
+          uint64_t *bar = !v ? &sh.k_full[j & 1] : land ? &sh.v_land[j & 1] : &sh.v_full[j & 1];
+          const uint32_t parity = land ? (j & 1 ? lands[1]++ : lands[0]++) : j >> 1;
+          if (j & 1) {
+            last_bar[v][1] = bar;
+            last_parity[v][1] = parity & 1u;
+          } else {
+            last_bar[v][0] = bar;
+            last_parity[v][0] = parity & 1u;
+          }
+          if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(__popc(there) * bytes));
+          __syncwarp();
+          if (slot >= 0) {
+#pragma unroll
+            for (int blk = 0; blk < D / 64; ++blk)
+              tma_load_3d(dst + blk * C::BLOCK + lane * p.box * 128, v ? &v_map : &k_map, bar, 64 * blk, h, slot, policy);
+          }
+        }
+      }
+      if (!ok) {  // the copies on their way end before the CTA does
+        int never = 0;
+        for (int v = 0; v < 2; ++v)
+          for (int i = 0; i < 2; ++i)
+            if (last_bar[v][i]) mbar_wait_bounded(last_bar[v][i], last_parity[v][i], &never);
+      }
+    } else if (warp == AP_MMA_WARP + 2) {
+      // --- values that are not finite, in tiles that not every row sees whole ----
+      int uses[2] = {0, 0};
+      for (int j = 0; j < nt; ++j) {
+        if (!partial(j)) continue;
+        const int st = j & 1;
+        if (!__all_sync(0xffffffffu, wait(&sh.v_land[st], st ? uses[1]++ : uses[0]++))) break;
+        bool odd = false;
+        const uint4 *v = reinterpret_cast<const uint4 *>(smem + C::V_OFF + st * C::OPERAND);
+#pragma unroll 4
+        for (int i = lane; i < C::OPERAND / 16; i += 32) {
+          const uint4 q = v[i];
+          const uint32_t e[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) odd |= (e[k] & 0x7F80u) == 0x7F80u || (e[k] & 0x7F800000u) == 0x7F800000u;
+        }
+        odd = __any_sync(0xffffffffu, odd);
+        if (lane == 0) {
+          sh.odd[st][0] = odd;
+          mbar_arrive(&sh.v_full[st]);
+        }
+        __syncwarp();
+      }
     }
   } else {
     // --- the tiles ------------------------------------------------------------
@@ -531,11 +662,6 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prompt_kernel(const ApArgs
         return -1;
       }
       return Q4 ? (blk * a.H + h) * a.block_size + off : blk * a.block_size + off;
-    };
-    // Whether some row of the CTA does not see all of tile j.
-    auto partial = [&](int j) {
-      const int j0 = attn_tile_start<AP_TILE>(R, j), jl = j0 + AP_TILE - 1;
-      return jl > p_lo || (a.window && !(j0 > p_hi - a.window || jl < a.sinks));
     };
     auto room = [&](int x) {  // wait until the half-tile's place is free
       const int j = x >> 3;
@@ -588,14 +714,26 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prompt_kernel(const ApArgs
           if (!ok) break;
         }
         const uint32_t there = __ballot_sync(0xffffffffu, slot >= 0);
-        if ((x & 4) && lane == 0) sh.there[j & 1][x & 3] = there;
+        if (!(x & 4) && lane == 0) sh.there[j & 3][x & 3] = there;
         const uint8_t *src = static_cast<const uint8_t *>(x & 4 ? a.v : a.k) + (size_t)h * D * 2 + ch * 16;
-        const uint32_t dst = smem_addr(smem + (x & 4 ? C::V_OFF : C::K_OFF) + (j & 1) * C::OPERAND) + (ch >> 3) * C::BLOCK;
+        // Row i PER + t0 of the group, piece ch ^ (row & 7): the rows' turns are
+        // a lane's own (t0) and the instruction's (a constant).
+        const uint32_t dst = smem_addr(smem + (x & 4 ? C::V_OFF : C::K_OFF) + (j & 1) * C::OPERAND) + (ch >> 3) * C::BLOCK +
+                             (32 * (x & 3) + t0) * 128 + ((ch ^ t0) & 7) * 16;
+        const uint32_t at = (uint32_t)max(slot, 0);
+        if (there == 0xffffffffu) {
 #pragma unroll
-        for (int i = 0; i < 32 / PER; ++i) {
-          const int t = i * PER + t0, row = 32 * (x & 3) + t;
-          const int s = __shfl_sync(0xffffffffu, slot, t);
-          ap_cp_async_16(dst + row * 128 + ((ch & 7) ^ (row & 7)) * 16, src + (size_t)(uint32_t)max(s, 0) * stride, s >= 0);
+          for (int i = 0; i < 32 / PER; ++i) {
+            const uint32_t s = __shfl_sync(0xffffffffu, at, i * PER + t0);
+            ap_cp_async_16((dst ^ ((i * PER & 7) * 16)) + i * PER * 128, src + (size_t)s * stride, true);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32 / PER; ++i) {
+            const uint32_t s = __shfl_sync(0xffffffffu, at, i * PER + t0);
+            ap_cp_async_16((dst ^ ((i * PER & 7) * 16)) + i * PER * 128, src + (size_t)s * stride,
+                           (there >> (i * PER + t0)) & 1u);
+          }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
         if (done <= x - 2 * AP_LOADERS) {  // two groups of this warp stay in flight
@@ -658,12 +796,12 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prompt_kernel(const ApArgs
             *reinterpret_cast<uint4 *>(at + (piece ^ (row & 7)) * 16) = turn ? o[k ^ 2] : o[k];
           }
         }
-        if (x & 4) {
-          odd = __any_sync(0xffffffffu, odd) && partial(j);
-          if (lane == 0) {
+        odd = __any_sync(0xffffffffu, odd);
+        if (lane == 0) {
+          if (x & 4)
             sh.odd[j & 1][x & 3] = odd;
-            sh.there[j & 1][x & 3] = there;
-          }
+          else
+            sh.there[j & 3][x & 3] = there;
         }
         arrive(x);
       }
@@ -678,20 +816,45 @@ __global__ void __launch_bounds__(AP_THREADS, 1) attn_prompt_kernel(const ApArgs
   if (tid == 0 && sh.abort) raise_status(a.status, MLORA_DEV_TIMEOUT);
 }
 
-template <bool Q4, int D>
-static cudaError_t launch_prompt(const ApArgs &p, cudaStream_t s) {
+typedef CUresult (*ApEncodeFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                               const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                               CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// A cache as (D, H, slots): boxes of 64 elements of one head in `box` slots,
+// 128-byte swizzle.
+static bool ap_map(CUtensorMap *map, const void *base, const AttnArgs &a, int box) {
+  static ApEncodeFn fn = nullptr;
+  if (!fn) {
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<ApEncodeFn>(p);
+    if (!fn) return false;
+  }
+  cuuint64_t dims[3] = {(cuuint64_t)a.D, (cuuint64_t)a.H, (cuuint64_t)a.num_blocks * a.block_size};
+  cuuint64_t strides[2] = {(cuuint64_t)a.D * 2, (cuuint64_t)a.H * a.D * 2};
+  cuuint32_t boxes[3] = {64, 1, (cuuint32_t)box};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, boxes, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int MODE, int D>
+static cudaError_t launch_prompt(const ApArgs &p, const CUtensorMap &k_map, const CUtensorMap &v_map, cudaStream_t s) {
   static int done[64] = {0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   constexpr int smem = ApCfg<D>::SMEM;
   if (dev >= 64 || !done[dev]) {
-    e = cudaFuncSetAttribute(attn_prompt_kernel<Q4, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    e = cudaFuncSetAttribute(attn_prompt_kernel<MODE, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     if (dev < 64) done[dev] = 1;
   }
   const long long grid = (long long)p.n_rt * p.a.H * p.a.B;
-  return launch_pdl(attn_prompt_kernel<Q4, D>, dim3((unsigned)grid), dim3(AP_THREADS), smem, s, p);
+  return launch_pdl(attn_prompt_kernel<MODE, D>, dim3((unsigned)grid), dim3(AP_THREADS), smem, s, p, k_map, v_map);
 }
 
 cudaError_t launch_attn_prompt(const AttnArgs &a, bool q4, cudaStream_t s) {
@@ -707,8 +870,17 @@ cudaError_t launch_attn_prompt(const AttnArgs &a, bool q4, cudaStream_t s) {
   const long long rq = (long long)a.rows_per_req * p.G;
   p.halves = rq > 128 ? 2 : 1;
   p.n_rt = (int)((rq + 128 * p.halves - 1) / (128 * p.halves));
-  if (a.D == 128) return q4 ? launch_prompt<true, 128>(p, s) : launch_prompt<false, 128>(p, s);
-  return q4 ? launch_prompt<true, 64>(p, s) : launch_prompt<false, 64>(p, s);
+  // Boxes: the largest power of two that divides a page (and the tile).  Below
+  // 8 positions a box would be less than a 1024-byte swizzle pattern.
+  p.box = a.block_size & -a.block_size;
+  if (p.box > AP_TILE) p.box = AP_TILE;
+  CUtensorMap km = {}, vm = {};
+  if (q4) return a.D == 128 ? launch_prompt<AP_CODES, 128>(p, km, vm, s) : launch_prompt<AP_CODES, 64>(p, km, vm, s);
+  if (p.box >= 8) {
+    if (!ap_map(&km, a.k, a, p.box) || !ap_map(&vm, a.v, a, p.box)) return cudaErrorInvalidValue;
+    return a.D == 128 ? launch_prompt<AP_BOXES, 128>(p, km, vm, s) : launch_prompt<AP_BOXES, 64>(p, km, vm, s);
+  }
+  return a.D == 128 ? launch_prompt<AP_PIECES, 128>(p, km, vm, s) : launch_prompt<AP_PIECES, 64>(p, km, vm, s);
 }
 
 }  // namespace mlora
