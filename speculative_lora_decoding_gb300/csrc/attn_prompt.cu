@@ -7,17 +7,18 @@
 // the group) in order, so the heads that share a cache head share its tiles.
 // For each tile of 128 positions and each half of 128 rows
 //   S = Q K^T          operands in shared memory, S in tensor memory;
-//   P = 2^(S - m)      one thread per row, registers, back over S;
+//   P = 2^(S - m)      two threads per row (half the positions each), in
+//                      registers, back over S;
 //   O += P V           P from tensor memory, O stays in tensor memory.
 // The halves alternate: the tensor cores work on one while the threads of the
 // other take exponentials.  The running maximum m moves (and O is rescaled,
 // in tensor memory) only when a score exceeds it by 8 in log2 units; until
 // then a tile is one pass over its scores.
 //
-// Warps 0-3 and 4-7 hold the rows of the two halves, warp 8 issues the MMAs,
-// warps 9-11 bring the tiles into 128-byte-swizzled rows (K read K-major, V
+// Warps 0-7 and 8-15 hold the rows of the two halves, warp 16 issues the MMAs,
+// warps 17-19 bring the tiles into 128-byte-swizzled rows (K read K-major, V
 // along its rows), in one of three ways:
-//   boxes   bf16 cache whose pages are multiples of 8 positions: warp 9 copies
+//   boxes   bf16 cache whose pages are multiples of 8 positions: warp 17 copies
 //           boxes of a page's positions by TMA, a lane to a box;
 //   pieces  other pages: all three gather 16-byte pieces;
 //   codes   4-bit cache: all three expand codes to fp16 on the way, exactly.
@@ -28,9 +29,9 @@ namespace mlora {
 
 constexpr int AP_TILE = 128;
 constexpr int AP_GROUPS = 4;   // of 32 positions in a tile
-constexpr int AP_LOADERS = 3;  // 12 warps leave 168 registers to a thread, which the scores' threads need
-constexpr int AP_MMA_WARP = 8;
-constexpr int AP_WARPS = 9 + AP_LOADERS;
+constexpr int AP_LOADERS = 3;
+constexpr int AP_MMA_WARP = 16;
+constexpr int AP_WARPS = AP_MMA_WARP + 1 + AP_LOADERS;
 constexpr int AP_THREADS = 32 * AP_WARPS;
 constexpr float AP_SLACK = 8.f;
 constexpr float AP_NONE = -__builtin_huge_valf();
@@ -43,7 +44,8 @@ struct ApCfg {
   static constexpr int K_OFF = 2 * OPERAND;             // two stages
   static constexpr int V_OFF = 4 * OPERAND;             // two stages
   static constexpr int BAR_OFF = 6 * OPERAND;
-  static constexpr int SMEM = BAR_OFF + 512 + 1024;     // and the alignment
+  static constexpr int X_OFF = BAR_OFF + 512;           // what a row's two threads tell each other
+  static constexpr int SMEM = X_OFF + 2 * 2 * 128 * 4 + 1024;  // and the alignment
 };
 
 enum { AP_BOXES = 0, AP_PIECES = 1, AP_CODES = 2 };
@@ -63,7 +65,7 @@ struct ApArgs {
   uint32_t G_magic;
   int extent, bs_shift;
   int n_rt, halves;  // row tiles per (request, cache head), of halves * 128 rows
-  int box;           // positions of a TMA box
+  int box_log2;      // positions of a TMA box
 };
 
 __device__ __forceinline__ void ap_cp_async_16(uint32_t dst, const void *src, bool there) {
@@ -240,16 +242,16 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
 
   const int halves = n_rows > 128 ? 2 : 1;
   if (tid == 0) {
-    mbar_init(&sh.q_full, 128 * halves);
+    mbar_init(&sh.q_full, 256 * halves);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.k_full[i], MODE == AP_BOXES ? 1 : AP_GROUPS);
-      mbar_init(&sh.v_full[i], MODE == AP_BOXES ? 1 : AP_GROUPS);
+      mbar_init(&sh.v_full[i], MODE == AP_BOXES ? 2 : AP_GROUPS);
       mbar_init(&sh.v_land[i], 1);
       mbar_init(&sh.k_empty[i], 1);
       mbar_init(&sh.v_empty[i], 1);
       mbar_init(&sh.s_full[i], 1);
-      mbar_init(&sh.p_full[i], 128);
+      mbar_init(&sh.p_full[i], 256);
       mbar_init(&sh.o_full[i], 1);
     }
     mbar_init(&sh.fin, 1);
@@ -282,19 +284,20 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
   };
   auto is_odd = [&](int j) {  // (V of tile j has landed)
     const int *f = sh.odd[j & 1];
-    return MODE == AP_BOXES ? f[0] != 0 : (f[0] | f[1] | f[2] | f[3]) != 0;
+    return MODE == AP_BOXES ? (f[0] | f[1]) != 0 : (f[0] | f[1] | f[2] | f[3]) != 0;
   };
 
-  if (warp < 8) {
-    const int half = warp >> 2;
+  if (warp < AP_MMA_WARP) {
+    // side: positions 64 side .. of a tile, elements D/2 side .. of O
+    const int half = warp >> 3, side = (warp >> 2) & 1;
     if (half < halves) {
-      // --- a row per thread --------------------------------------------------
+      // --- two threads per row --------------------------------------------------
       const int row = (warp & 3) * 32 + lane, r = r0 + half * 128 + row;
       const bool valid = r < rq;
       const int rc = min(r, rq - 1), t = div_heads(rc, p.G, p.G_magic);
       const long long pos = p0 + t;
-      const int hi = (int)min(pos, 0x7fffffffll);  // sees j <= hi, j > lo or j < sinks
-      const int lo = a.window ? (int)max(min(pos - a.window, 0x7fffffffll), -1ll) : -1;
+      const int hi = (int)min(pos, 0x7ffffffell);  // sees j <= hi, j > lo or j < sinks
+      const int lo = a.window ? (int)max(min(pos - a.window, 0x7ffffffell), -1ll) : -1;
       const int hi_first = __shfl_sync(0xffffffffu, hi, 0), lo_last = __shfl_sync(0xffffffffu, lo, 31);
       float mul = fabsf(a.scale_log2);  // (a negative scale's sign goes into q)
       const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;
@@ -317,8 +320,8 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
           down = __uint_as_float((254u - e) << 23);
           mul *= __uint_as_float(e << 23);
         }
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
+#pragma unroll 4
+        for (int i = side * (D / 16); i < (side + 1) * (D / 16); ++i) {
           uint4 v = valid ? __ldg(reinterpret_cast<const uint4 *>(src) + i) : make_uint4(0, 0, 0, 0);
           v = make_uint4(v.x ^ flip, v.y ^ flip, v.z ^ flip, v.w ^ flip);
           if (Q4) {
@@ -337,9 +340,12 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
       const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
       const uint32_t ts = tmem + lanes + 128 * half, to = tmem + lanes + 256 + 128 * half;
       float m = AP_NONE, l = 0.f;
+      float *mine = reinterpret_cast<float *>(smem + C::X_OFF) + (half * 2 + side) * 128 + row;
+      const float *theirs = reinterpret_cast<float *>(smem + C::X_OFF) + (half * 2 + (side ^ 1)) * 128 + row;
+      const int pair_bar = 1 + half * 4 + (warp & 3);  // the two warps of 32 rows
       auto rescale_o = [&](float corr) {
 #pragma unroll 1
-        for (int i = 0; i < D; i += 16) {
+        for (int i = side * (D / 2); i < (side + 1) * (D / 2); i += 16) {
           uint32_t o[16];
           tmem_ld_x16(to + i, o);
           tmem_ld_wait16(o);
@@ -362,37 +368,31 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
         const bool odd = part && is_odd(j);
         const bool edge = (there[0] & there[1] & there[2] & there[3]) != 0xffffffffu || jl > hi_first ||
                           (a.window && !(j0 > lo_last || jl < a.sinks));
-        auto sees = [&](int jj, uint32_t bits) {
-          const int jp = j0 + jj;
-          return ((bits >> (jj & 31)) & 1u) && jp <= hi && (jp > lo || jp < a.sinks);
+        // The positions 32 ch .. 32 ch + 31 of the tile that this row sees, as bits.
+        auto seen = [&](int ch) {
+          auto below = [](int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u; };
+          const int at = j0 + 32 * ch;
+          return there[ch] & below(hi - at + 1) & (~below(lo - at + 1) | below(min(a.sinks, 1 << 30) - at));
         };
-        // First the row's maximum, over all scores, 32 at a time while the next
-        // are on their way; then the weights, with no decision among them.  P
-        // goes over the first scores, which are the last to be looked at and
-        // still in registers then.
+        // The row's maximum first, then the weights with no decision among
+        // them.  P goes over scores that both warps have read by then.
         uint32_t s0[32], s1[32];
         auto hide = [&](uint32_t (&x)[32], int ch) {
-          const uint32_t bits = there[ch];
+          const uint32_t bits = seen(ch);
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (!sees(32 * ch + i, bits)) x[i] = 0xff800000u;  // -infinity
+          for (int i = 0; i < 32; ++i) x[i] = (bits >> i) & 1u ? x[i] : 0xff800000u;  // -infinity
         };
-        tmem_ld_x32(ts + 64, s0);
+        tmem_ld_x32(ts + 64 * side, s0);
         tmem_ld_wait32(s0);
-        tmem_ld_x32(ts + 96, s1);
-        if (edge) hide(s0, 2);
+        tmem_ld_x32(ts + 64 * side + 32, s1);
+        if (edge) hide(s0, 2 * side);
         float mx = max_x32(s0, AP_NONE);
         tmem_ld_wait32(s1);
-        tmem_ld_x32(ts, s0);
-        if (edge) hide(s1, 3);
+        if (edge) hide(s1, 2 * side + 1);
         mx = max_x32(s1, mx);
-        tmem_ld_wait32(s0);
-        tmem_ld_x32(ts + 32, s1);
-        if (edge) hide(s0, 0);
-        mx = max_x32(s0, mx);
-        tmem_ld_wait32(s1);
-        if (edge) hide(s1, 1);
-        mx = max_x32(s1, mx);
+        *mine = mx;
+        named_bar_sync(pair_bar, 64);
+        mx = fmaxf(mx, *theirs);
         float base = m == AP_NONE ? 0.f : m;
         const float d = fmaf(mx, mul, -base);
         const bool far = mx > AP_NONE && (d > AP_SLACK || m == AP_NONE);
@@ -413,25 +413,16 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
           for (int i = 0; i < 32; ++i) v[i] = exp2_weight(v[i]);
 #pragma unroll
           for (int i = 0; i < 32; i += 2) pk[i / 2] = ap_pack2<Q4>(v[i], v[i + 1]);
-          if (!odd) tmem_st_x16(ts + 16 * ch, pk);
+          if (!odd) tmem_st_x16(ts + 32 * side + 16 * ch, pk);
           return sum_x32(v);
         };
-        float sum = weights(s0, 0);
-        tmem_ld_x32(ts + 64, s0);
-        sum += weights(s1, 1);
-        tmem_ld_wait32(s0);
-        tmem_ld_x32(ts + 96, s1);
-        if (edge) hide(s0, 2);
-        sum += weights(s0, 2);
-        tmem_ld_wait32(s1);
-        if (edge) hide(s1, 3);
-        sum += weights(s1, 3);
-        l += sum;
+        l += weights(s0, 0);
+        l += weights(s1, 1);
         if (odd) {
           // Values that are not finite and that some rows do not see: the
           // product would bring 0 times them to those rows.  This tile is added
           // up here, a position at a time (the MMA warp leaves it out).
-          for (int d0 = 0; d0 < D; d0 += 32) {
+          for (int d0 = side * (D / 2); d0 < (side + 1) * (D / 2); d0 += 32) {
             uint32_t o[32];
             if (j > 0) {
               tmem_ld_x32(to + d0, o);
@@ -444,7 +435,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
               uint32_t s1;
               tmem_ld_x1(ts + jj, s1);
               asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(s1) : : "memory");
-              if (sees(jj, there[jj >> 5])) {
+              if ((seen(jj >> 5) >> (jj & 31)) & 1u) {
                 const float w = exp2_weight(fmaf(__uint_as_float(s1), mul, -base));
                 const uint8_t *v = smem + C::V_OFF + (j & 1) * C::OPERAND + (d0 >> 6) * C::BLOCK + jj * 128;
 #pragma unroll
@@ -472,10 +463,13 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
       if (ok) ok = __all_sync(0xffffffffu, wait(&sh.o_full[half], 0));
       if (ok) {
         tc_fence_after_sync();
+        *mine = l;
+        named_bar_sync(pair_bar, 64);
+        l += *theirs;
         const float w = l != 0.f ? a.v_unit / l : 0.f;
         uint4 *dst = reinterpret_cast<uint4 *>(out_row(rc));
-#pragma unroll
-        for (int i = 0; i < D; i += 32) {
+#pragma unroll 1
+        for (int i = side * (D / 2); i < (side + 1) * (D / 2); i += 32) {
           uint32_t o[32];
           tmem_ld_x32(to + i, o);
           tmem_ld_wait32(o);
@@ -493,6 +487,8 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
         }
         tc_fence_before_sync();
       }
+      // The other warp of these rows may be waiting for this one; it gives up at its next wait.
+      if (!ok) named_bar_arrive(pair_bar, 64);
     }
   } else if (warp == AP_MMA_WARP) {
     // --- the MMAs, issued by lane 0 -------------------------------------------
@@ -520,8 +516,9 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
     __syncwarp();
     for (int j = 0; j < nt && ok; ++j) {
       for (int half = 0; half < halves && ok; ++half) {
-        ok = wait(&sh.p_full[half], j) && wait(&sh.v_full[j & 1], j >> 1);
-        if (j + 1 < nt) ok = ok && wait(&sh.k_full[(j + 1) & 1], (j + 1) >> 1);
+        // (P comes last as a rule)
+        ok = wait(&sh.v_full[j & 1], j >> 1) && (j + 1 == nt || wait(&sh.k_full[(j + 1) & 1], (j + 1) >> 1)) &&
+             wait(&sh.p_full[half], j);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after_sync();
@@ -549,10 +546,10 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
   } else if (MODE == AP_BOXES) {
     if (warp == AP_MMA_WARP + 1) {
       // --- the tiles, by TMA: lane i brings the tile's box i ---------------------
-      const int n_box = AP_TILE / p.box, bytes = p.box * 128 * (D / 64);
+      const int lb = p.box_log2, n_box = AP_TILE >> lb, bytes = (128 * (D / 64)) << lb;
       auto slot_of = [&](int j) {  // the box's first slot; -1: none
         if (j >= nt || lane >= n_box) return -1;
-        const int pos = attn_tile_start<AP_TILE>(R, j) + lane * p.box;
+        const int pos = attn_tile_start<AP_TILE>(R, j) + (lane << lb);
         if (pos >= (j < R.st ? R.sink : R.n)) return -1;
         const int page = p.bs_shift >= 0 ? pos >> p.bs_shift : pos / a.block_size;
         const int blk = __ldg(a.block_table + (size_t)b * a.max_blocks + page);
@@ -580,10 +577,10 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
           if (there != all) {  // boxes that are not read are zeros
             for (uint32_t left = all & ~there; left; left &= left - 1) {
               const int i = __ffs(left) - 1;
-              for (int e = lane; e < p.box * 8 * (D / 64); e += 32) {
-                const int blk = e / (p.box * 8), at = e - blk * p.box * 8;
-                *reinterpret_cast<uint4 *>(dst + blk * C::BLOCK + i * p.box * 128 + at * 16) = make_uint4(0, 0, 0, 0);
-              }
+              for (int e = lane; e < (8 << lb); e += 32)
+#pragma unroll
+                for (int blk = 0; blk < D / 64; ++blk)
+                  *reinterpret_cast<uint4 *>(dst + blk * C::BLOCK + ((i << lb) * 8 + e) * 16) = make_uint4(0, 0, 0, 0);
             }
             fence_proxy_async_smem();
           }
@@ -591,7 +588,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
             uint32_t bits = 0xffffffffu;
             if (there != all) {
               bits = 0;
-              for (int i = 0; i < 32; ++i) bits |= ((there >> ((32 * lane + i) / p.box)) & 1u) << i;
+              for (int i = 0; i < 32; ++i) bits |= ((there >> ((32 * lane + i) >> lb)) & 1u) << i;
             }
             sh.there[j & 3][lane] = bits;
           }
@@ -608,11 +605,12 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
             last_parity[v][0] = parity & 1u;
           }
           if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(__popc(there) * bytes));
+          if (lane == 1 && v && !land) mbar_arrive(bar);  // (for the two warps that look tiles over)
           __syncwarp();
           if (slot >= 0) {
 #pragma unroll
             for (int blk = 0; blk < D / 64; ++blk)
-              tma_load_3d(dst + blk * C::BLOCK + lane * p.box * 128, v ? &v_map : &k_map, bar, 64 * blk, h, slot, policy);
+              tma_load_3d(dst + blk * C::BLOCK + ((lane << lb) * 128), v ? &v_map : &k_map, bar, 64 * blk, h, slot, policy);
           }
         }
       }
@@ -622,7 +620,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
           for (int i = 0; i < 2; ++i)
             if (last_bar[v][i]) mbar_wait_bounded(last_bar[v][i], last_parity[v][i], &never);
       }
-    } else if (warp == AP_MMA_WARP + 2) {
+    } else {
       // --- values that are not finite, in tiles that not every row sees whole ----
       int uses[2] = {0, 0};
       for (int j = 0; j < nt; ++j) {
@@ -631,8 +629,9 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
         if (!__all_sync(0xffffffffu, wait(&sh.v_land[st], st ? uses[1]++ : uses[0]++))) break;
         bool odd = false;
         const uint4 *v = reinterpret_cast<const uint4 *>(smem + C::V_OFF + st * C::OPERAND);
-#pragma unroll 4
-        for (int i = lane; i < C::OPERAND / 16; i += 32) {
+        const int who = warp - AP_MMA_WARP - 2;
+#pragma unroll 8
+        for (int i = 32 * who + lane; i < C::OPERAND / 16; i += 64) {
           const uint4 q = v[i];
           const uint32_t e[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
@@ -640,7 +639,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
         }
         odd = __any_sync(0xffffffffu, odd);
         if (lane == 0) {
-          sh.odd[st][0] = odd;
+          sh.odd[st][who] = odd;
           mbar_arrive(&sh.v_full[st]);
         }
         __syncwarp();
@@ -872,12 +871,12 @@ cudaError_t launch_attn_prompt(const AttnArgs &a, bool q4, cudaStream_t s) {
   p.n_rt = (int)((rq + 128 * p.halves - 1) / (128 * p.halves));
   // Boxes: the largest power of two that divides a page (and the tile).  Below
   // 8 positions a box would be less than a 1024-byte swizzle pattern.
-  p.box = a.block_size & -a.block_size;
-  if (p.box > AP_TILE) p.box = AP_TILE;
+  p.box_log2 = 0;
+  while (p.box_log2 < 7 && a.block_size % (2 << p.box_log2) == 0) ++p.box_log2;
   CUtensorMap km = {}, vm = {};
   if (q4) return a.D == 128 ? launch_prompt<AP_CODES, 128>(p, km, vm, s) : launch_prompt<AP_CODES, 64>(p, km, vm, s);
-  if (p.box >= 8) {
-    if (!ap_map(&km, a.k, a, p.box) || !ap_map(&vm, a.v, a, p.box)) return cudaErrorInvalidValue;
+  if (p.box_log2 >= 3) {
+    if (!ap_map(&km, a.k, a, 1 << p.box_log2) || !ap_map(&vm, a.v, a, 1 << p.box_log2)) return cudaErrorInvalidValue;
     return a.D == 128 ? launch_prompt<AP_BOXES, 128>(p, km, vm, s) : launch_prompt<AP_BOXES, 64>(p, km, vm, s);
   }
   return a.D == 128 ? launch_prompt<AP_PIECES, 128>(p, km, vm, s) : launch_prompt<AP_PIECES, 64>(p, km, vm, s);
