@@ -508,40 +508,40 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
       mma_commit(&sh.s_full[half]);
       if (half == halves - 1) mma_commit(&sh.k_empty[j & 1]);
     };
-    bool ok = wait(&sh.q_full, 0) && wait(&sh.k_full[0], 0);
-    ok = __all_sync(0xffffffffu, ok);
-    tc_fence_after_sync();
-    if (ok && lane == 0)
-      for (int half = 0; half < halves; ++half) scores(0, half);
-    __syncwarp();
-    for (int j = 0; j < nt && ok; ++j) {
-      for (int half = 0; half < halves && ok; ++half) {
-        // (P comes last as a rule)
-        ok = wait(&sh.v_full[j & 1], j >> 1) && (j + 1 == nt || wait(&sh.k_full[(j + 1) & 1], (j + 1) >> 1)) &&
-             wait(&sh.p_full[half], j);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        tc_fence_after_sync();
-        if (lane == 0) {
-          if (!(partial(j) && is_odd(j))) {
-            const uint64_t v = v0 + (j & 1) * STEP;
+    // One thread: what it spends between a barrier's completion and the next
+    // MMA is time in which the tensor cores wait.
+    if (lane == 0) {
+      auto ready = [&](uint64_t *bar, uint32_t parity) { return mbar_try_wait(bar, parity & 1u) || wait(bar, parity); };
+      bool ok = ready(&sh.q_full, 0) && ready(&sh.k_full[0], 0);
+      tc_fence_after_sync();
+      if (ok)
+        for (int half = 0; half < halves; ++half) scores(0, half);
+      for (int j = 0; j < nt && ok; ++j) {
+        const bool more = j + 1 < nt;
+        ok = ready(&sh.v_full[j & 1], j >> 1) && (!more || ready(&sh.k_full[(j + 1) & 1], (j + 1) >> 1));
+        const bool skip = ok && partial(j) && is_odd(j);
+        const uint64_t v = v0 + (j & 1) * STEP;
+        for (int half = 0; half < halves && ok; ++half) {
+          ok = ready(&sh.p_full[half], j);
+          if (!ok) break;
+          tc_fence_after_sync();
+          if (!skip) {
 #pragma unroll
             for (int kk = 0; kk < AP_TILE / 16; ++kk)
               mma_f16_ts(tmem + 256 + 128 * half, tmem + 128 * half + 8 * kk, v + kk * 128, ID_O, j > 0 || kk > 0);
           }
           if (half == halves - 1) mma_commit(&sh.v_empty[j & 1]);
-          if (j + 1 < nt)
+          if (more)
             scores(j + 1, half);
           else
             mma_commit(&sh.o_full[half]);
         }
-        __syncwarp();
       }
-    }
-    if (!ok) {  // what was issued ends before the tensor memory goes back
-      int never = 0;
-      if (lane == 0) mma_commit(&sh.fin);
-      mbar_wait_bounded(&sh.fin, 0, &never);
+      if (!ok) {  // what was issued ends before the tensor memory goes back
+        int never = 0;
+        mma_commit(&sh.fin);
+        mbar_wait_bounded(&sh.fin, 0, &never);
+      }
     }
   } else if (MODE == AP_BOXES) {
     if (warp == AP_MMA_WARP + 1) {
