@@ -38,8 +38,12 @@ constexpr float AP_NONE = -__builtin_huge_valf();
 
 template <int D>
 struct ApCfg {
-  static constexpr int BLOCK = AP_TILE * 128;           // 128 rows of 64 elements, 128-byte swizzle
-  static constexpr int OPERAND = BLOCK * (D / 64);      // 128 rows of D elements
+  // An operand's 128 rows of D elements: groups of 8 rows, in each the row's
+  // 64-element blocks side by side as 1024-byte swizzle patterns, so that any
+  // multiple of 8 positions with all their elements is one run of memory and
+  // one TMA box.
+  static constexpr int GROUP = 1024 * (D / 64);
+  static constexpr int OPERAND = AP_TILE / 8 * GROUP;
   static constexpr int Q_OFF = 0;                       // two halves
   static constexpr int K_OFF = 2 * OPERAND;             // two stages
   static constexpr int V_OFF = 4 * OPERAND;             // two stages
@@ -58,6 +62,12 @@ struct ApShared {
   int odd[2][AP_GROUPS];         // per V stage, tiles that not every row sees whole: some V is not finite
 };
 static_assert(sizeof(ApShared) <= 512, "ApShared");
+
+// Byte offset of a row's 16-byte piece in an operand.
+template <int D>
+__device__ __forceinline__ int ap_at(int row, int piece) {
+  return (row >> 3) * ApCfg<D>::GROUP + (piece >> 3) * 1024 + (row & 7) * 128 + ((piece ^ row) & 7) * 16;
+}
 
 struct ApArgs {
   AttnArgs a;
@@ -168,17 +178,30 @@ __device__ __forceinline__ float sum_x32(const float (&v)[32]) {
   return a + b;
 }
 
-// V's tile as the second product's B operand: 16 positions (K) by D elements
-// (N), N contiguous: rows of 64 elements (128 bytes, swizzled), 8 positions
-// 1024 bytes apart (stride offset), the next 64 elements a block further
-// (leading offset).
-__device__ __forceinline__ uint64_t smem_desc_nmajor_sw128(uint32_t saddr, uint32_t block_bytes) {
+// Q's and K's operands, K-major: the groups of 8 rows are the stride offset
+// apart, the blocks are stepped over by address.
+template <int D>
+__device__ __forceinline__ uint64_t ap_desc_k_major(uint32_t saddr) {
   uint64_t d = 0;
   d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
-  d |= (uint64_t)(block_bytes >> 4) << 16;  // leading byte offset
-  d |= (uint64_t)(1024 >> 4) << 32;         // stride byte offset
-  d |= (uint64_t)1 << 46;                   // descriptor version
-  d |= (uint64_t)2 << 61;                   // 128-byte swizzle
+  d |= (uint64_t)1 << 16;                              // leading byte offset (unused)
+  d |= (uint64_t)(ApCfg<D>::GROUP >> 4) << 32;         // stride byte offset
+  d |= (uint64_t)1 << 46;                              // descriptor version
+  d |= (uint64_t)2 << 61;                              // 128-byte swizzle
+  return d;
+}
+
+// V's tile as the second product's B operand: 16 positions (K) by D elements
+// (N), N contiguous: 8 positions are the stride offset apart, the next 64
+// elements the leading offset.
+template <int D>
+__device__ __forceinline__ uint64_t ap_desc_n_major(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)(1024 >> 4) << 16;                    // leading byte offset
+  d |= (uint64_t)(ApCfg<D>::GROUP >> 4) << 32;         // stride byte offset
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
   return d;
 }
 
@@ -303,7 +326,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
       const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;
       {
         const uint16_t *src = a.y + (size_t)(b * T + t) * a.ld + a.q_col + (size_t)(h * p.G + rc - t * p.G) * D;
-        uint8_t *dst = smem + C::Q_OFF + half * C::OPERAND + row * 128;
+        uint8_t *dst = smem + C::Q_OFF + half * C::OPERAND;
         float down = 1.f;
         if (Q4) {
           // fp16 relative to the row's largest magnitude (a power of two, given
@@ -331,7 +354,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
               w[k] = ap_pack2<true>(__uint_as_float(w[k] << 16) * down, __uint_as_float(w[k] & 0xFFFF0000u) * down);
             v = make_uint4(w[0], w[1], w[2], w[3]);
           }
-          *reinterpret_cast<uint4 *>(dst + (i >> 3) * C::BLOCK + ((i & 7) ^ (row & 7)) * 16) = v;
+          *reinterpret_cast<uint4 *>(dst + ap_at<D>(row, i)) = v;
         }
       }
       fence_proxy_async_smem();
@@ -437,10 +460,10 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
               asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(s1) : : "memory");
               if ((seen(jj >> 5) >> (jj & 31)) & 1u) {
                 const float w = exp2_weight(fmaf(__uint_as_float(s1), mul, -base));
-                const uint8_t *v = smem + C::V_OFF + (j & 1) * C::OPERAND + (d0 >> 6) * C::BLOCK + jj * 128;
+                const uint8_t *v = smem + C::V_OFF + (j & 1) * C::OPERAND;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                  const uint4 q = *reinterpret_cast<const uint4 *>(v + ((((d0 & 32) >> 3) + k) ^ (jj & 7)) * 16);
+                  const uint4 q = *reinterpret_cast<const uint4 *>(v + ap_at<D>(jj, (d0 >> 3) + k));
                   const uint32_t e[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
                   for (int i = 0; i < 4; ++i) {
@@ -492,17 +515,15 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
     }
   } else if (warp == AP_MMA_WARP) {
     // --- the MMAs, issued by lane 0 -------------------------------------------
-    const uint64_t q0 = smem_desc_kmajor_sw128(smem_addr(smem + C::Q_OFF)),
-                   k0 = smem_desc_kmajor_sw128(smem_addr(smem + C::K_OFF)),
-                   v0 = smem_desc_nmajor_sw128(smem_addr(smem + C::V_OFF), C::BLOCK);
+    const uint64_t q0 = ap_desc_k_major<D>(smem_addr(smem + C::Q_OFF)), k0 = ap_desc_k_major<D>(smem_addr(smem + C::K_OFF)),
+                   v0 = ap_desc_n_major<D>(smem_addr(smem + C::V_OFF));
     constexpr uint32_t ID_S = ap_idesc<Q4>(AP_TILE, false), ID_O = ap_idesc<Q4>(D, true);
     constexpr uint32_t STEP = C::OPERAND >> 4;  // in a descriptor's address units
     auto scores = [&](int j, int half) {
       const uint64_t q = q0 + half * STEP, k = k0 + (j & 1) * STEP;
 #pragma unroll
       for (int ks = 0; ks < D / 16; ++ks) {
-        constexpr uint32_t B16 = C::BLOCK >> 4;
-        const uint32_t off = (ks >> 2) * B16 + (ks & 3) * 2;
+        const uint32_t off = (ks >> 2) * (1024 >> 4) + (ks & 3) * 2;
         mma_bf16_ss(tmem + 128 * half, q + off, k + off, ID_S, ks > 0);
       }
       mma_commit(&sh.s_full[half]);
@@ -528,7 +549,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
           if (!skip) {
 #pragma unroll
             for (int kk = 0; kk < AP_TILE / 16; ++kk)
-              mma_f16_ts(tmem + 256 + 128 * half, tmem + 128 * half + 8 * kk, v + kk * 128, ID_O, j > 0 || kk > 0);
+              mma_f16_ts(tmem + 256 + 128 * half, tmem + 128 * half + 8 * kk, v + kk * (2 * C::GROUP >> 4), ID_O, j > 0 || kk > 0);
           }
           if (half == halves - 1) mma_commit(&sh.v_empty[j & 1]);
           if (more)
@@ -577,10 +598,8 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
           if (there != all) {  // boxes that are not read are zeros
             for (uint32_t left = all & ~there; left; left &= left - 1) {
               const int i = __ffs(left) - 1;
-              for (int e = lane; e < (8 << lb); e += 32)
-#pragma unroll
-                for (int blk = 0; blk < D / 64; ++blk)
-                  *reinterpret_cast<uint4 *>(dst + blk * C::BLOCK + ((i << lb) * 8 + e) * 16) = make_uint4(0, 0, 0, 0);
+              uint4 *at = reinterpret_cast<uint4 *>(dst + ((i << lb) >> 3) * C::GROUP);
+              for (int e = lane; e < (D / 8) << lb; e += 32) at[e] = make_uint4(0, 0, 0, 0);
             }
             fence_proxy_async_smem();
           }
@@ -607,11 +626,8 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
           if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(__popc(there) * bytes));
           if (lane == 1 && v && !land) mbar_arrive(bar);  // (for the two warps that look tiles over)
           __syncwarp();
-          if (slot >= 0) {
-#pragma unroll
-            for (int blk = 0; blk < D / 64; ++blk)
-              tma_load_3d(dst + blk * C::BLOCK + ((lane << lb) * 128), v ? &v_map : &k_map, bar, 64 * blk, h, slot, policy);
-          }
+          if (slot >= 0)
+            tma_load_5d(dst + ((lane << lb) >> 3) * C::GROUP, v ? &v_map : &k_map, bar, 0, 0, 0, slot >> 3, h, policy);
         }
       }
       if (!ok) {  // the copies on their way end before the CTA does
@@ -688,9 +704,9 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
           __syncwarp();
           bool odd = false;
           if (partial(j)) {
-            const uint8_t *v = smem + C::V_OFF + (j & 1) * C::OPERAND + (32 * (x & 3) + lane) * 128;
+            const uint8_t *v = smem + C::V_OFF + (j & 1) * C::OPERAND;
             for (int piece = 0; piece < CH; ++piece) {
-              const uint4 q = *reinterpret_cast<const uint4 *>(v + (piece >> 3) * C::BLOCK + (piece & 7) * 16);
+              const uint4 q = *reinterpret_cast<const uint4 *>(v + ap_at<D>(32 * (x & 3) + lane, piece));
               const uint32_t e[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
               for (int k = 0; k < 4; ++k) odd |= (e[k] & 0x7F80u) == 0x7F80u || (e[k] & 0x7F800000u) == 0x7F800000u;
@@ -717,20 +733,20 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
         const uint8_t *src = static_cast<const uint8_t *>(x & 4 ? a.v : a.k) + (size_t)h * D * 2 + ch * 16;
         // Row i PER + t0 of the group, piece ch ^ (row & 7): the rows' turns are
         // a lane's own (t0) and the instruction's (a constant).
-        const uint32_t dst = smem_addr(smem + (x & 4 ? C::V_OFF : C::K_OFF) + (j & 1) * C::OPERAND) + (ch >> 3) * C::BLOCK +
-                             (32 * (x & 3) + t0) * 128 + ((ch ^ t0) & 7) * 16;
+        const uint32_t dst = smem_addr(smem + (x & 4 ? C::V_OFF : C::K_OFF) + (j & 1) * C::OPERAND) +
+                             ap_at<D>(32 * (x & 3) + t0, ch);
         const uint32_t at = (uint32_t)max(slot, 0);
         if (there == 0xffffffffu) {
 #pragma unroll
           for (int i = 0; i < 32 / PER; ++i) {
             const uint32_t s = __shfl_sync(0xffffffffu, at, i * PER + t0);
-            ap_cp_async_16((dst ^ ((i * PER & 7) * 16)) + i * PER * 128, src + (size_t)s * stride, true);
+            ap_cp_async_16((dst ^ ((i * PER & 7) * 16)) + (i * PER >> 3) * C::GROUP + (i * PER & 7) * 128, src + (size_t)s * stride, true);
           }
         } else {
 #pragma unroll
           for (int i = 0; i < 32 / PER; ++i) {
             const uint32_t s = __shfl_sync(0xffffffffu, at, i * PER + t0);
-            ap_cp_async_16((dst ^ ((i * PER & 7) * 16)) + i * PER * 128, src + (size_t)s * stride,
+            ap_cp_async_16((dst ^ ((i * PER & 7) * 16)) + (i * PER >> 3) * C::GROUP + (i * PER & 7) * 128, src + (size_t)s * stride,
                            (there >> (i * PER + t0)) & 1u);
           }
         }
@@ -787,12 +803,10 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
           }
           // Pieces 4 cl .. 4 cl + 3 of the row; lanes of the upper 64 elements
           // start two pieces later, so that eight lanes' stores differ in bank.
-          uint8_t *at = dst + (cl >> 1) * C::BLOCK + row * 128;
           const bool turn = cl & 2;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const int piece = 4 * (cl & 1) + (turn ? k ^ 2 : k);
-            *reinterpret_cast<uint4 *>(at + (piece ^ (row & 7)) * 16) = turn ? o[k ^ 2] : o[k];
+            *reinterpret_cast<uint4 *>(dst + ap_at<D>(row, 4 * cl + (turn ? k ^ 2 : k))) = turn ? o[k ^ 2] : o[k];
           }
         }
         odd = __any_sync(0xffffffffu, odd);
@@ -819,8 +833,8 @@ typedef CUresult (*ApEncodeFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, v
                                const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-// A cache as (D, H, slots): boxes of 64 elements of one head in `box` slots,
-// 128-byte swizzle.
+// A cache as (64 elements, 8 slots, D / 64 blocks, slots / 8, H): a box is one
+// head's elements of 8 n slots, in the order of an operand's groups.
 static bool ap_map(CUtensorMap *map, const void *base, const AttnArgs &a, int box) {
   static ApEncodeFn fn = nullptr;
   if (!fn) {
@@ -831,11 +845,12 @@ static bool ap_map(CUtensorMap *map, const void *base, const AttnArgs &a, int bo
       fn = reinterpret_cast<ApEncodeFn>(p);
     if (!fn) return false;
   }
-  cuuint64_t dims[3] = {(cuuint64_t)a.D, (cuuint64_t)a.H, (cuuint64_t)a.num_blocks * a.block_size};
-  cuuint64_t strides[2] = {(cuuint64_t)a.D * 2, (cuuint64_t)a.H * a.D * 2};
-  cuuint32_t boxes[3] = {64, 1, (cuuint32_t)box};
-  cuuint32_t estr[3] = {1, 1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, boxes, estr,
+  const cuuint64_t row = (cuuint64_t)a.H * a.D * 2;
+  cuuint64_t dims[5] = {64, 8, (cuuint64_t)a.D / 64, (cuuint64_t)a.num_blocks * a.block_size / 8, (cuuint64_t)a.H};
+  cuuint64_t strides[4] = {row, 128, 8 * row, (cuuint64_t)a.D * 2};
+  cuuint32_t boxes[5] = {64, 8, (cuuint32_t)a.D / 64, (cuuint32_t)box / 8, 1};
+  cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void *>(base), dims, strides, boxes, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
