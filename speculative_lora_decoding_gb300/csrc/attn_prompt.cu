@@ -54,12 +54,12 @@ struct ApCfg {
 
 enum { AP_BOXES = 0, AP_PIECES = 1, AP_CODES = 2 };
 
-struct ApShared {
+struct __align__(16) ApShared {
   uint64_t q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], v_land[2], s_full[2], p_full[2], o_full[2], fin;
   uint32_t tmem;
   int abort;
-  uint32_t there[4][AP_GROUPS];  // of the last tiles: positions whose slot is in the cache
-  int odd[2][AP_GROUPS];         // per V stage, tiles that not every row sees whole: some V is not finite
+  alignas(16) uint32_t there[4][AP_GROUPS];  // of the last tiles: positions whose slot is in the cache
+  int odd[2][AP_GROUPS];         // per V stage: some V that not every row sees is not finite
 };
 static_assert(sizeof(ApShared) <= 512, "ApShared");
 
@@ -265,7 +265,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
 
   const int halves = n_rows > 128 ? 2 : 1;
   if (tid == 0) {
-    mbar_init(&sh.q_full, 256 * halves);
+    mbar_init(&sh.q_full, 8 * halves);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.k_full[i], MODE == AP_BOXES ? 1 : AP_GROUPS);
@@ -274,10 +274,12 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
       mbar_init(&sh.k_empty[i], 1);
       mbar_init(&sh.v_empty[i], 1);
       mbar_init(&sh.s_full[i], 1);
-      mbar_init(&sh.p_full[i], 256);
+      mbar_init(&sh.p_full[i], 8);
       mbar_init(&sh.o_full[i], 1);
     }
     mbar_init(&sh.fin, 1);
+#pragma unroll
+    for (int i = 0; i < 2 * AP_GROUPS; ++i) (&sh.odd[0][0])[i] = 0;
     sh.abort = 0;
     fence_mbar_init();
   }
@@ -305,9 +307,9 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
     const int j0 = attn_tile_start<AP_TILE>(R, j), jl = j0 + AP_TILE - 1;
     return jl > p_lo || (a.window && !(j0 > p_hi - a.window || jl < a.sinks));
   };
-  auto is_odd = [&](int j) {  // (V of tile j has landed)
-    const int *f = sh.odd[j & 1];
-    return MODE == AP_BOXES ? (f[0] | f[1]) != 0 : (f[0] | f[1] | f[2] | f[3]) != 0;
+  auto is_odd = [&](int stage) {  // (V of the stage's tile has landed)
+    const int4 f = *reinterpret_cast<const int4 *>(sh.odd[stage]);
+    return (f.x | f.y | f.z | f.w) != 0;
   };
 
   if (warp < AP_MMA_WARP) {
@@ -358,7 +360,8 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
         }
       }
       fence_proxy_async_smem();
-      mbar_arrive(&sh.q_full);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.q_full);
 
       const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
       const uint32_t ts = tmem + lanes + 128 * half, to = tmem + lanes + 256 + 128 * half;
@@ -388,7 +391,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
         tc_fence_after_sync();
         const int j0 = attn_tile_start<AP_TILE>(R, j), jl = j0 + AP_TILE - 1;
         const uint32_t *there = sh.there[j & 3];
-        const bool odd = part && is_odd(j);
+        const bool odd = part && is_odd(j & 1);
         const bool edge = (there[0] & there[1] & there[2] & there[3]) != 0xffffffffu || jl > hi_first ||
                           (a.window && !(j0 > lo_last || jl < a.sinks));
         // The positions 32 ch .. 32 ch + 31 of the tile that this row sees, as bits.
@@ -481,7 +484,8 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
         }
         tmem_st_wait();
         tc_fence_before_sync();
-        mbar_arrive(&sh.p_full[half]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.p_full[half]);
       }
       if (ok) ok = __all_sync(0xffffffffu, wait(&sh.o_full[half], 0));
       if (ok) {
@@ -514,55 +518,71 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
       if (!ok) named_bar_arrive(pair_bar, 64);
     }
   } else if (warp == AP_MMA_WARP) {
-    // --- the MMAs, issued by lane 0 -------------------------------------------
+    // --- the MMAs --------------------------------------------------------------
+    // What this warp spends between a barrier's completion and the next MMA is
+    // time in which the tensor cores wait: the whole warp runs the loop, on
+    // values that are the same in all lanes (one lane alone took 70 cycles to
+    // hand over an MMA that runs for 64), with the stages constants.
     const uint64_t q0 = ap_desc_k_major<D>(smem_addr(smem + C::Q_OFF)), k0 = ap_desc_k_major<D>(smem_addr(smem + C::K_OFF)),
                    v0 = ap_desc_n_major<D>(smem_addr(smem + C::V_OFF));
     constexpr uint32_t ID_S = ap_idesc<Q4>(AP_TILE, false), ID_O = ap_idesc<Q4>(D, true);
     constexpr uint32_t STEP = C::OPERAND >> 4;  // in a descriptor's address units
-    auto scores = [&](int j, int half) {
-      const uint64_t q = q0 + half * STEP, k = k0 + (j & 1) * STEP;
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    auto ready = [&](uint64_t *bar, uint32_t parity) { return mbar_try_wait(bar, parity) || wait(bar, parity); };
+    // (issued by one elected lane)
+    auto scores = [&](int stage, int half) {
+      const uint64_t q = q0 + half * STEP, k = k0 + stage * STEP;
 #pragma unroll
       for (int ks = 0; ks < D / 16; ++ks) {
         const uint32_t off = (ks >> 2) * (1024 >> 4) + (ks & 3) * 2;
-        mma_bf16_ss(tmem + 128 * half, q + off, k + off, ID_S, ks > 0);
+        mma_bf16_ss(tm + 128 * half, q + off, k + off, ID_S, ks > 0);
       }
       mma_commit(&sh.s_full[half]);
-      if (half == halves - 1) mma_commit(&sh.k_empty[j & 1]);
+      if (half == halves - 1) mma_commit(&sh.k_empty[stage]);
     };
-    // One thread: what it spends between a barrier's completion and the next
-    // MMA is time in which the tensor cores wait.
-    if (lane == 0) {
-      auto ready = [&](uint64_t *bar, uint32_t parity) { return mbar_try_wait(bar, parity & 1u) || wait(bar, parity); };
-      bool ok = ready(&sh.q_full, 0) && ready(&sh.k_full[0], 0);
+    bool ok = ready(&sh.q_full, 0) && ready(&sh.k_full[0], 0);
+    tc_fence_after_sync();
+    if (ok && elect_lane()) {
+      scores(0, 0);
+      if (halves == 2) scores(0, 1);
+    }
+    __syncwarp();
+    // Tile j in stage st: P V, and the scores of the next tile over P.
+    auto half_step = [&](int j, int st, int half, bool skip, bool more) {
+      if (!ready(&sh.p_full[half], st)) return false;
       tc_fence_after_sync();
-      if (ok)
-        for (int half = 0; half < halves; ++half) scores(0, half);
-      for (int j = 0; j < nt && ok; ++j) {
-        const bool more = j + 1 < nt;
-        ok = ready(&sh.v_full[j & 1], j >> 1) && (!more || ready(&sh.k_full[(j + 1) & 1], (j + 1) >> 1));
-        const bool skip = ok && partial(j) && is_odd(j);
-        const uint64_t v = v0 + (j & 1) * STEP;
-        for (int half = 0; half < halves && ok; ++half) {
-          ok = ready(&sh.p_full[half], j);
-          if (!ok) break;
-          tc_fence_after_sync();
-          if (!skip) {
+      if (elect_lane()) {
+        if (!skip) {
+          const uint64_t v = v0 + st * STEP;
 #pragma unroll
-            for (int kk = 0; kk < AP_TILE / 16; ++kk)
-              mma_f16_ts(tmem + 256 + 128 * half, tmem + 128 * half + 8 * kk, v + kk * (2 * C::GROUP >> 4), ID_O, j > 0 || kk > 0);
-          }
-          if (half == halves - 1) mma_commit(&sh.v_empty[j & 1]);
-          if (more)
-            scores(j + 1, half);
-          else
-            mma_commit(&sh.o_full[half]);
+          for (int kk = 0; kk < AP_TILE / 16; ++kk)
+            mma_f16_ts(tm + 256 + 128 * half, tm + 128 * half + 8 * kk, v + kk * (2 * C::GROUP >> 4), ID_O, kk > 0 ? 1 : j > 0);
         }
+        if (half == halves - 1) mma_commit(&sh.v_empty[st]);
+        if (more)
+          scores(st ^ 1, half);
+        else
+          mma_commit(&sh.o_full[half]);
       }
-      if (!ok) {  // what was issued ends before the tensor memory goes back
-        int never = 0;
-        mma_commit(&sh.fin);
-        mbar_wait_bounded(&sh.fin, 0, &never);
-      }
+      __syncwarp();
+      return true;
+    };
+    auto step = [&](int j, int st) {
+      const uint32_t parity = (j >> 1) & 1;
+      const bool more = j + 1 < nt;
+      if (!ready(&sh.v_full[st], parity) || (more && !ready(&sh.k_full[st ^ 1], st ? parity ^ 1 : parity))) return false;
+      const bool skip = is_odd(st);
+      return half_step(j, st, 0, skip, more) && (halves == 1 || half_step(j, st, 1, skip, more));
+    };
+    for (int j = 0; j < nt && ok; j += 2) {
+      ok = step(j, 0);
+      if (ok && j + 1 < nt) ok = step(j + 1, 1);
+    }
+    if (!ok) {  // what was issued ends before the tensor memory goes back
+      int never = 0;
+      if (elect_lane()) mma_commit(&sh.fin);
+      __syncwarp();
+      mbar_wait_bounded(&sh.fin, 0, &never);
     }
   } else if (MODE == AP_BOXES) {
     if (warp == AP_MMA_WARP + 1) {
@@ -624,6 +644,8 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
             last_parity[v][0] = parity & 1u;
           }
           if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(__popc(there) * bytes));
+          if (lane < 2 && v && !land) sh.odd[j & 1][lane] = 0;
+          __syncwarp();
           if (lane == 1 && v && !land) mbar_arrive(bar);  // (for the two warps that look tiles over)
           __syncwarp();
           if (slot >= 0)
@@ -809,7 +831,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
             *reinterpret_cast<uint4 *>(dst + ap_at<D>(row, 4 * cl + (turn ? k ^ 2 : k))) = turn ? o[k ^ 2] : o[k];
           }
         }
-        odd = __any_sync(0xffffffffu, odd);
+        odd = __any_sync(0xffffffffu, odd) && partial(j);
         if (lane == 0) {
           if (x & 4)
             sh.odd[j & 1][x & 3] = odd;
