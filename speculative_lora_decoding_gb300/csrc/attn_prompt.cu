@@ -49,7 +49,8 @@ struct ApCfg {
   static constexpr int V_OFF = 4 * OPERAND;             // two stages
   static constexpr int BAR_OFF = 6 * OPERAND;
   static constexpr int X_OFF = BAR_OFF + 512;           // what a row's two threads tell each other
-  static constexpr int SMEM = X_OFF + 2 * 2 * 128 * 4 + 1024;  // and the alignment
+  static constexpr int E_OFF = X_OFF + 2 * 2 * 128 * 4;  // q's powers of two (4-bit cache)
+  static constexpr int SMEM = E_OFF + 2 * 128 * 4 + 1024;  // and the alignment
 };
 
 enum { AP_BOXES = 0, AP_PIECES = 1, AP_CODES = 2 };
@@ -318,45 +319,48 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
     if (half < halves) {
       // --- two threads per row --------------------------------------------------
       const int row = (warp & 3) * 32 + lane, r = r0 + half * 128 + row;
-      const bool valid = r < rq;
       const int rc = min(r, rq - 1), t = div_heads(rc, p.G, p.G_magic);
       const long long pos = p0 + t;
       const int hi = (int)min(pos, 0x7ffffffell);  // sees j <= hi, j > lo or j < sinks
       const int lo = a.window ? (int)max(min(pos - a.window, 0x7ffffffell), -1ll) : -1;
       const int hi_first = __shfl_sync(0xffffffffu, hi, 0), lo_last = __shfl_sync(0xffffffffu, lo, 31);
-      float mul = fabsf(a.scale_log2);  // (a negative scale's sign goes into q)
-      const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;
+      const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;  // a negative scale's sign goes into q
+      float *q_exp = reinterpret_cast<float *>(smem + C::E_OFF) + half * 128;
       {
-        const uint16_t *src = a.y + (size_t)(b * T + t) * a.ld + a.q_col + (size_t)(h * p.G + rc - t * p.G) * D;
+        // A warp brings 16 rows, D / 8 lanes to a row, all of them asked for at once.
+        constexpr int LR = D / 8, PER = 32 / LR, N = 16 / PER;
         uint8_t *dst = smem + C::Q_OFF + half * C::OPERAND;
-        float down = 1.f;
-        if (Q4) {
-          // fp16 relative to the row's largest magnitude (a power of two, given
-          // back to the scores): exact but for entries 2^-14 below it.
-          uint32_t mx = 0;
+        const int first = (warp & 7) * 16 + lane / LR, piece = lane & (LR - 1);
+        uint4 q[N];
 #pragma unroll
-          for (int i = 0; i < D / 8; ++i) {
-            const uint4 v = __ldg(reinterpret_cast<const uint4 *>(src) + i);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        for (int i = 0; i < N; ++i) {
+          const int rr = r0 + half * 128 + first + i * PER;
+          q[i] = make_uint4(0, 0, 0, 0);
+          if (rr < rq) {
+            const int tt = div_heads(rr, p.G, p.G_magic);
+            q[i] = __ldg(reinterpret_cast<const uint4 *>(a.y + (size_t)(b * T + tt) * a.ld + a.q_col +
+                                                         (size_t)(h * p.G + rr - tt * p.G) * D) + piece);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          uint32_t w[4] = {q[i].x ^ flip, q[i].y ^ flip, q[i].z ^ flip, q[i].w ^ flip};
+          if (Q4) {
+            // fp16 relative to the row's largest magnitude (a power of two, given
+            // back to the scores): exact but for entries 2^-14 below it.
+            uint32_t mx = 0;
 #pragma unroll
             for (int k = 0; k < 4; ++k) mx = max(mx, max(w[k] & 0x7FFFu, (w[k] >> 16) & 0x7FFFu));
-          }
-          const uint32_t e = min(max(mx >> 7, 1u), 253u);
-          down = __uint_as_float((254u - e) << 23);
-          mul *= __uint_as_float(e << 23);
-        }
-#pragma unroll 4
-        for (int i = side * (D / 16); i < (side + 1) * (D / 16); ++i) {
-          uint4 v = valid ? __ldg(reinterpret_cast<const uint4 *>(src) + i) : make_uint4(0, 0, 0, 0);
-          v = make_uint4(v.x ^ flip, v.y ^ flip, v.z ^ flip, v.w ^ flip);
-          if (Q4) {
-            uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int k = 1; k < LR; k <<= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, k));
+            const uint32_t e = min(max(mx >> 7, 1u), 253u);
+            const float down = __uint_as_float((254u - e) << 23);
+            if (piece == 0) q_exp[first + i * PER] = __uint_as_float(e << 23);
 #pragma unroll
             for (int k = 0; k < 4; ++k)
               w[k] = ap_pack2<true>(__uint_as_float(w[k] << 16) * down, __uint_as_float(w[k] & 0xFFFF0000u) * down);
-            v = make_uint4(w[0], w[1], w[2], w[3]);
           }
-          *reinterpret_cast<uint4 *>(dst + ap_at<D>(row, i)) = v;
+          *reinterpret_cast<uint4 *>(dst + ap_at<D>(first + i * PER, piece)) = make_uint4(w[0], w[1], w[2], w[3]);
         }
       }
       fence_proxy_async_smem();
@@ -365,7 +369,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
 
       const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
       const uint32_t ts = tmem + lanes + 128 * half, to = tmem + lanes + 256 + 128 * half;
-      float m = AP_NONE, l = 0.f;
+      float m = AP_NONE, l = 0.f, mul = fabsf(a.scale_log2);
       float *mine = reinterpret_cast<float *>(smem + C::X_OFF) + (half * 2 + side) * 128 + row;
       const float *theirs = reinterpret_cast<float *>(smem + C::X_OFF) + (half * 2 + (side ^ 1)) * 128 + row;
       const int pair_bar = 1 + half * 4 + (warp & 3);  // the two warps of 32 rows
@@ -389,6 +393,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
           break;
         }
         tc_fence_after_sync();
+        if (Q4 && j == 0) mul *= q_exp[row];  // (the scores of all rows are there, so their q was)
         const int j0 = attn_tile_start<AP_TILE>(R, j), jl = j0 + AP_TILE - 1;
         const uint32_t *there = sh.there[j & 3];
         const bool odd = part && is_odd(j & 1);
@@ -494,23 +499,33 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
         named_bar_sync(pair_bar, 64);
         l += *theirs;
         const float w = l != 0.f ? a.v_unit / l : 0.f;
-        uint4 *dst = reinterpret_cast<uint4 *>(out_row(rc));
+        // Through the place of q, which no MMA reads any more, so that 8 (D = 64:
+        // 4) lanes write a row's half.
+        uint8_t *stage = smem + C::Q_OFF + half * C::OPERAND;
 #pragma unroll 1
         for (int i = side * (D / 2); i < (side + 1) * (D / 2); i += 32) {
           uint32_t o[32];
           tmem_ld_x32(to + i, o);
           tmem_ld_wait32(o);
-          if (valid) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              uint32_t x[4];
+          for (int k = 0; k < 4; ++k) {
+            uint32_t x[4];
 #pragma unroll
-              for (int q = 0; q < 4; ++q)
-                x[q] = w != 0.f ? ap_pack2<false>(__uint_as_float(o[8 * k + 2 * q]) * w, __uint_as_float(o[8 * k + 2 * q + 1]) * w)
-                                : 0u;
-              dst[i / 8 + k] = make_uint4(x[0], x[1], x[2], x[3]);
-            }
+            for (int q = 0; q < 4; ++q)
+              x[q] = w != 0.f ? ap_pack2<false>(__uint_as_float(o[8 * k + 2 * q]) * w, __uint_as_float(o[8 * k + 2 * q + 1]) * w)
+                              : 0u;
+            *reinterpret_cast<uint4 *>(stage + ap_at<D>(row, i / 8 + k)) = make_uint4(x[0], x[1], x[2], x[3]);
           }
+        }
+        __syncwarp();
+        constexpr int LR = D / 16, PER = 32 / LR;
+        const int piece = side * LR + (lane & (LR - 1));
+#pragma unroll 4
+        for (int i = 0; i < 32; i += PER) {
+          const int rr = (warp & 3) * 32 + i + lane / LR;
+          if (r0 + half * 128 + rr < rq)
+            reinterpret_cast<uint4 *>(out_row(r0 + half * 128 + rr))[piece] =
+                *reinterpret_cast<const uint4 *>(stage + ap_at<D>(rr, piece));
         }
         tc_fence_before_sync();
       }
