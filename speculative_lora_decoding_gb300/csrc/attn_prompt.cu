@@ -7,21 +7,22 @@
 // the group) in order, so the heads that share a cache head share its tiles.
 // For each tile of 128 positions and each half of 128 rows
 //   S = Q K^T          operands in shared memory, S in tensor memory;
-//   P = 2^(S - m)      two threads per row (half the positions each), in
-//                      registers, back over S;
+//   P = 2^(S - m)      one thread per row, in registers, back over S;
 //   O += P V           P from tensor memory, O stays in tensor memory.
-// The halves alternate: the tensor cores work on one while the threads of the
-// other take exponentials.  The running maximum m moves (and O is rescaled,
+// Each half's tile is handed back and forth in two parts of 64 positions, so
+// that the scores of the next part are there when a thread is done with one
+// (with whole tiles, the way from P through the MMAs to the next scores stood
+// between a half's exponentials: 3600 cycles a tile against ... now).  The running maximum m moves (and O is rescaled,
 // in tensor memory) only when a score exceeds it by 8 in log2 units; until
 // then a tile is one pass over its scores.
 //
-// Warps 0-7 and 8-15 hold the rows of the two halves, warp 16 issues the MMAs,
-// warps 17-19 bring the tiles into 128-byte-swizzled rows (K read K-major, V
+// Warps 0-3 and 4-7 hold the rows of the two halves, warp 8 issues the MMAs, the
+// others bring the tiles into 128-byte-swizzled rows (K read K-major, V
 // along its rows), in one of three ways:
-//   boxes   bf16 cache whose pages are multiples of 8 positions: warp 17 copies
+//   boxes   bf16 cache whose pages are multiples of 8 positions: warp 9 copies
 //           boxes of a page's positions by TMA, a lane to a box;
-//   pieces  other pages: all three gather 16-byte pieces;
-//   codes   4-bit cache: all three expand codes to fp16 on the way, exactly.
+//   pieces  other pages: a gather of 16-byte pieces;
+//   codes   4-bit cache: codes are expanded to fp16 on the way, exactly.
 #include "attn_common.cuh"
 #include "e2m1.cuh"
 
@@ -29,10 +30,7 @@ namespace mlora {
 
 constexpr int AP_TILE = 128;
 constexpr int AP_GROUPS = 4;   // of 32 positions in a tile
-constexpr int AP_LOADERS = 3;
-constexpr int AP_MMA_WARP = 16;
-constexpr int AP_WARPS = AP_MMA_WARP + 1 + AP_LOADERS;
-constexpr int AP_THREADS = 32 * AP_WARPS;
+constexpr int AP_MMA_WARP = 8;
 constexpr float AP_SLACK = 8.f;
 constexpr float AP_NONE = -__builtin_huge_valf();
 
@@ -48,15 +46,17 @@ struct ApCfg {
   static constexpr int K_OFF = 2 * OPERAND;             // two stages
   static constexpr int V_OFF = 4 * OPERAND;             // two stages
   static constexpr int BAR_OFF = 6 * OPERAND;
-  static constexpr int X_OFF = BAR_OFF + 512;           // what a row's two threads tell each other
-  static constexpr int E_OFF = X_OFF + 2 * 2 * 128 * 4;  // q's powers of two (4-bit cache)
+  static constexpr int E_OFF = BAR_OFF + 512;           // q's powers of two (4-bit cache)
   static constexpr int SMEM = E_OFF + 2 * 128 * 4 + 1024;  // and the alignment
 };
 
 enum { AP_BOXES = 0, AP_PIECES = 1, AP_CODES = 2 };
+// Warps that bring tiles: with boxes one copies and two look the tiles over.
+__host__ __device__ constexpr int ap_loaders(int mode) { return mode == AP_BOXES ? 3 : 7; }
+__host__ __device__ constexpr int ap_threads(int mode) { return 32 * (AP_MMA_WARP + 1 + ap_loaders(mode)); }
 
 struct __align__(16) ApShared {
-  uint64_t q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], v_land[2], s_full[2], p_full[2], o_full[2], fin;
+  uint64_t q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], v_land[2], s_full[2][2], p_full[2][2], o_done[2], fin;
   uint32_t tmem;
   int abort;
   alignas(16) uint32_t there[4][AP_GROUPS];  // of the last tiles: positions whose slot is in the cache
@@ -87,23 +87,49 @@ __device__ __forceinline__ void ap_cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Wait for the loads whose registers are named, so that no use moves before it.
-__device__ __forceinline__ void tmem_ld_wait32(uint32_t (&r)[32]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
-                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
-                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
-               :
-               : "memory");
+// Tensor memory to registers, load and wait in one statement: between the two
+// the registers are not yet what the compiler takes them for (it may move or
+// spill them).
+__device__ __forceinline__ void tmem_get(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "{\n\ttcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15},"
+      " [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;\n\t}"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
 }
 
-__device__ __forceinline__ void tmem_ld_wait16(uint32_t (&r)[16]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
-               :
-               : "memory");
+__device__ __forceinline__ void tmem_get(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "{\n\ttcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,"
+      "%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
+      "tcgen05.wait::ld.sync.aligned;\n\t}"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_get(uint32_t taddr, uint32_t (&r)[64]) {
+  asm volatile(
+      "{\n\ttcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,"
+      "%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,"
+      "%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];\n\t"
+      "tcgen05.wait::ld.sync.aligned;\n\t}"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]),
+        "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]),
+        "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]),
+        "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]),
+        "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+      : "r"(taddr)
+      : "memory");
 }
 
 __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[16]) {
@@ -139,7 +165,7 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uin
 }
 
 // v = x * mul + add, two at a time.
-__device__ __forceinline__ void fma_x32(float (&v)[32], const uint32_t (&x)[32], float mul, float add) {
+__device__ __forceinline__ void fma_x32(float (&v)[32], const uint32_t *x, float mul, float add) {
   uint64_t m2, a2;
   asm("mov.b64 %0, {%1, %1};" : "=l"(m2) : "f"(mul));
   asm("mov.b64 %0, {%1, %1};" : "=l"(a2) : "f"(add));
@@ -151,11 +177,11 @@ __device__ __forceinline__ void fma_x32(float (&v)[32], const uint32_t (&x)[32],
     asm("mov.b64 {%0, %1}, %2;" : "=f"(v[i]), "=f"(v[i + 1]) : "l"(y));
   }
 }
-// The largest of y and 32 values (NaN left out).
-__device__ __forceinline__ float max_x32(const uint32_t (&x)[32], float y) {
-  float m[4];
+// The largest of 64 values (NaN left out).
+__device__ __forceinline__ float max_x64(const uint32_t (&x)[64]) {
+  float m[8];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
+  for (int k = 0; k < 8; ++k) {
     m[k] = __uint_as_float(x[8 * k + 7]);
 #pragma unroll
     for (int i = 0; i < 6; i += 2)
@@ -164,7 +190,11 @@ __device__ __forceinline__ float max_x32(const uint32_t (&x)[32], float y) {
           : "f"(__uint_as_float(x[8 * k + i])), "f"(__uint_as_float(x[8 * k + i + 1])));
     m[k] = fmaxf(m[k], __uint_as_float(x[8 * k + 6]));
   }
-  return fmaxf(fmaxf(m[0], m[1]), fmaxf(fmaxf(m[2], m[3]), y));
+#pragma unroll
+  for (int n = 4; n > 0; n >>= 1)
+#pragma unroll
+    for (int k = 0; k < n; ++k) m[k] = fmaxf(m[k], m[k + n]);
+  return m[0];
 }
 __device__ __forceinline__ float sum_x32(const float (&v)[32]) {
   uint64_t y[16];
@@ -228,10 +258,11 @@ __device__ __forceinline__ uint32_t ap_hmul2(uint32_t a, uint32_t b) {
 }
 
 template <int MODE, int D>
-__global__ void __launch_bounds__(AP_THREADS, 1)
+__global__ void __launch_bounds__(ap_threads(MODE), 1)
     attn_prompt_kernel(const ApArgs p, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
   using C = ApCfg<D>;
   constexpr bool Q4 = MODE == AP_CODES;
+  constexpr int LOADERS = ap_loaders(MODE);
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = align_smem_1024(smem_raw);
   ApShared &sh = *reinterpret_cast<ApShared *>(smem + C::BAR_OFF);
@@ -259,14 +290,14 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
     return a.out + ((size_t)(b * T + t) * a.Hq + h * p.G + r - t * p.G) * D;
   };
   if (nt == 0) {  // nothing to see: zeros
-    for (int i = tid; i < n_rows * (D / 8); i += AP_THREADS)
+    for (int i = tid; i < n_rows * (D / 8); i += ap_threads(MODE))
       reinterpret_cast<uint4 *>(out_row(r0 + i / (D / 8)))[i % (D / 8)] = make_uint4(0, 0, 0, 0);
     return;
   }
 
   const int halves = n_rows > 128 ? 2 : 1;
   if (tid == 0) {
-    mbar_init(&sh.q_full, 8 * halves);
+    mbar_init(&sh.q_full, 4 * halves);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.k_full[i], MODE == AP_BOXES ? 1 : AP_GROUPS);
@@ -274,9 +305,12 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
       mbar_init(&sh.v_land[i], 1);
       mbar_init(&sh.k_empty[i], 1);
       mbar_init(&sh.v_empty[i], 1);
-      mbar_init(&sh.s_full[i], 1);
-      mbar_init(&sh.p_full[i], 8);
-      mbar_init(&sh.o_full[i], 1);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        mbar_init(&sh.s_full[i][k], 1);
+        mbar_init(&sh.p_full[i][k], 4);
+      }
+      mbar_init(&sh.o_done[i], 1);
     }
     mbar_init(&sh.fin, 1);
 #pragma unroll
@@ -301,7 +335,8 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
     *abort = 1;
     return false;
   };
-  // S (and P over it) of half i at column 128 i, O at 256 + 128 i.
+  // S of half i at columns 128 i (first 64 positions of the tile) and 128 i + 64,
+  // P over each, O at 256 + 128 i.
 
   // Whether some row of the CTA does not see all of tile j.
   auto partial = [&](int j) {
@@ -314,10 +349,9 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
   };
 
   if (warp < AP_MMA_WARP) {
-    // side: positions 64 side .. of a tile, elements D/2 side .. of O
-    const int half = warp >> 3, side = (warp >> 2) & 1;
+    const int half = warp >> 2;
     if (half < halves) {
-      // --- two threads per row --------------------------------------------------
+      // --- a row per thread --------------------------------------------------
       const int row = (warp & 3) * 32 + lane, r = r0 + half * 128 + row;
       const int rc = min(r, rq - 1), t = div_heads(rc, p.G, p.G_magic);
       const long long pos = p0 + t;
@@ -327,10 +361,10 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
       const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;  // a negative scale's sign goes into q
       float *q_exp = reinterpret_cast<float *>(smem + C::E_OFF) + half * 128;
       {
-        // A warp brings 16 rows, D / 8 lanes to a row, all of them asked for at once.
-        constexpr int LR = D / 8, PER = 32 / LR, N = 16 / PER;
+        // A warp brings 32 rows, D / 8 lanes to a row, all of them asked for at once.
+        constexpr int LR = D / 8, PER = 32 / LR, N = 32 / PER;
         uint8_t *dst = smem + C::Q_OFF + half * C::OPERAND;
-        const int first = (warp & 7) * 16 + lane / LR, piece = lane & (LR - 1);
+        const int first = (warp & 3) * 32 + lane / LR, piece = lane & (LR - 1);
         uint4 q[N];
 #pragma unroll
         for (int i = 0; i < N; ++i) {
@@ -370,115 +404,116 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
       const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
       const uint32_t ts = tmem + lanes + 128 * half, to = tmem + lanes + 256 + 128 * half;
       float m = AP_NONE, l = 0.f, mul = fabsf(a.scale_log2);
-      float *mine = reinterpret_cast<float *>(smem + C::X_OFF) + (half * 2 + side) * 128 + row;
-      const float *theirs = reinterpret_cast<float *>(smem + C::X_OFF) + (half * 2 + (side ^ 1)) * 128 + row;
-      const int pair_bar = 1 + half * 4 + (warp & 3);  // the two warps of 32 rows
       auto rescale_o = [&](float corr) {
 #pragma unroll 1
-        for (int i = side * (D / 2); i < (side + 1) * (D / 2); i += 16) {
+        for (int i = 0; i < D; i += 16) {
           uint32_t o[16];
-          tmem_ld_x16(to + i, o);
-          tmem_ld_wait16(o);
+          tmem_get(to + i, o);
 #pragma unroll
           for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * corr);
           tmem_st_x16(to + i, o);
         }
       };
       bool ok = true;
-      for (int j = 0; j < nt; ++j) {
+      for (int i = 0; i < 2 * nt; ++i) {  // part i & 1 of tile i / 2
+        const int j = i >> 1, sub = i & 1;
         const bool part = partial(j);
-        ok = wait(&sh.s_full[half], j) && (!part || wait(&sh.v_full[j & 1], j >> 1));
+        ok = wait(&sh.s_full[half][sub], j) && (!part || wait(&sh.v_full[j & 1], j >> 1));
         if (!__all_sync(0xffffffffu, ok)) {
           ok = false;
           break;
         }
         tc_fence_after_sync();
-        if (Q4 && j == 0) mul *= q_exp[row];  // (the scores of all rows are there, so their q was)
-        const int j0 = attn_tile_start<AP_TILE>(R, j), jl = j0 + AP_TILE - 1;
-        const uint32_t *there = sh.there[j & 3];
+        if (Q4 && i == 0) mul *= q_exp[row];  // (the scores of all rows are there, so their q was)
+        const int j0 = attn_tile_start<AP_TILE>(R, j) + 64 * sub, jl = j0 + 63;
+        const uint32_t sc = ts + 64 * sub;
+        const uint32_t *there = sh.there[j & 3] + 2 * sub;
         const bool odd = part && is_odd(j & 1);
-        const bool edge = (there[0] & there[1] & there[2] & there[3]) != 0xffffffffu || jl > hi_first ||
+        const bool edge = (there[0] & there[1]) != 0xffffffffu || jl > hi_first ||
                           (a.window && !(j0 > lo_last || jl < a.sinks));
-        // The positions 32 ch .. 32 ch + 31 of the tile that this row sees, as bits.
+        // The positions 32 ch .. 32 ch + 31 of the part that this row sees, as bits.
         auto seen = [&](int ch) {
           auto below = [](int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u; };
           const int at = j0 + 32 * ch;
           return there[ch] & below(hi - at + 1) & (~below(lo - at + 1) | below(min(a.sinks, 1 << 30) - at));
         };
-        // The row's maximum first, then the weights with no decision among
-        // them.  P goes over scores that both warps have read by then.
-        uint32_t s0[32], s1[32];
-        auto hide = [&](uint32_t (&x)[32], int ch) {
-          const uint32_t bits = seen(ch);
+        // The row's maximum first, then the weights with no decision among them.
+        uint32_t s[64];
+        tmem_get(sc, s);
+        if (edge) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) x[i] = (bits >> i) & 1u ? x[i] : 0xff800000u;  // -infinity
-        };
-        tmem_ld_x32(ts + 64 * side, s0);
-        tmem_ld_wait32(s0);
-        tmem_ld_x32(ts + 64 * side + 32, s1);
-        if (edge) hide(s0, 2 * side);
-        float mx = max_x32(s0, AP_NONE);
-        tmem_ld_wait32(s1);
-        if (edge) hide(s1, 2 * side + 1);
-        mx = max_x32(s1, mx);
-        *mine = mx;
-        named_bar_sync(pair_bar, 64);
-        mx = fmaxf(mx, *theirs);
+          for (int ch = 0; ch < 2; ++ch) {
+            const uint32_t bits = seen(ch);
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              s[32 * ch + k] = (bits >> k) & 1u ? s[32 * ch + k] : 0xff800000u;  // -infinity
+          }
+        }
+        const float mx = max_x64(s);
         float base = m == AP_NONE ? 0.f : m;
         const float d = fmaf(mx, mul, -base);
         const bool far = mx > AP_NONE && (d > AP_SLACK || m == AP_NONE);
-        if (__any_sync(0xffffffffu, far)) {
+        const bool any_far = __any_sync(0xffffffffu, far);
+        // O is about to be touched: the product before must be done (the one
+        // before that is, since these scores came after it).
+        if ((any_far || odd) && i > 0) {
+          ok = __all_sync(0xffffffffu, wait(&sh.o_done[half], i - 1));
+          if (!ok) break;
+          tc_fence_after_sync();
+        }
+        if (any_far) {
           // The maximum of the rows that need it moves by a whole number, so
           // that what is summed so far scales exactly.
           const float by = far ? floorf(d) : 0.f;
           const float corr = far && m != AP_NONE ? exp2_weight(-by) : 1.f;
           if (far) m = base = base + by;
           l *= corr;
-          if (j > 0) rescale_o(corr);
+          if (i > 0) rescale_o(corr);
         }
-        auto weights = [&](uint32_t (&x)[32], int ch) {
+#pragma unroll
+        for (int ch = 0; ch < 2; ++ch) {
           float v[32];
           uint32_t pk[16];
-          fma_x32(v, x, mul, -base);
+          fma_x32(v, s + 32 * ch, mul, -base);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = exp2_weight(v[i]);
+          for (int k = 0; k < 32; ++k) v[k] = exp2_weight(v[k]);
 #pragma unroll
-          for (int i = 0; i < 32; i += 2) pk[i / 2] = ap_pack2<Q4>(v[i], v[i + 1]);
-          if (!odd) tmem_st_x16(ts + 32 * side + 16 * ch, pk);
-          return sum_x32(v);
-        };
-        l += weights(s0, 0);
-        l += weights(s1, 1);
+          for (int k = 0; k < 32; k += 2) pk[k / 2] = ap_pack2<Q4>(v[k], v[k + 1]);
+          if (!odd) tmem_st_x16(sc + 16 * ch, pk);
+          l += sum_x32(v);
+        }
         if (odd) {
           // Values that are not finite and that some rows do not see: the
           // product would bring 0 times them to those rows.  This tile is added
           // up here, a position at a time (the MMA warp leaves it out).
-          for (int d0 = side * (D / 2); d0 < (side + 1) * (D / 2); d0 += 32) {
+          for (int d0 = 0; d0 < D; d0 += 32) {
             uint32_t o[32];
-            if (j > 0) {
-              tmem_ld_x32(to + d0, o);
-              tmem_ld_wait32(o);
+            if (i > 0) {
+              tmem_get(to + d0, o);
             } else {
 #pragma unroll
               for (int k = 0; k < 32; ++k) o[k] = 0;
             }
-            for (int jj = 0; jj < AP_TILE; ++jj) {
+            for (int jj = 0; jj < 64; ++jj) {
               uint32_t s1;
-              tmem_ld_x1(ts + jj, s1);
-              asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(s1) : : "memory");
+              asm volatile(
+                  "{\n\ttcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n\ttcgen05.wait::ld.sync.aligned;\n\t}"
+                  : "=r"(s1)
+                  : "r"(sc + jj)
+                  : "memory");
               if ((seen(jj >> 5) >> (jj & 31)) & 1u) {
                 const float w = exp2_weight(fmaf(__uint_as_float(s1), mul, -base));
                 const uint8_t *v = smem + C::V_OFF + (j & 1) * C::OPERAND;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                  const uint4 q = *reinterpret_cast<const uint4 *>(v + ap_at<D>(jj, (d0 >> 3) + k));
+                  const uint4 q = *reinterpret_cast<const uint4 *>(v + ap_at<D>(64 * sub + jj, (d0 >> 3) + k));
                   const uint32_t e[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-                  for (int i = 0; i < 4; ++i) {
-                    const float x0 = Q4 ? f16_lo(e[i]) : __uint_as_float(e[i] << 16);
-                    const float x1 = Q4 ? f16_hi(e[i]) : __uint_as_float(e[i] & 0xFFFF0000u);
-                    o[8 * k + 2 * i] = __float_as_uint(fmaf(w, x0, __uint_as_float(o[8 * k + 2 * i])));
-                    o[8 * k + 2 * i + 1] = __float_as_uint(fmaf(w, x1, __uint_as_float(o[8 * k + 2 * i + 1])));
+                  for (int n = 0; n < 4; ++n) {
+                    const float x0 = Q4 ? f16_lo(e[n]) : __uint_as_float(e[n] << 16);
+                    const float x1 = Q4 ? f16_hi(e[n]) : __uint_as_float(e[n] & 0xFFFF0000u);
+                    o[8 * k + 2 * n] = __float_as_uint(fmaf(w, x0, __uint_as_float(o[8 * k + 2 * n])));
+                    o[8 * k + 2 * n + 1] = __float_as_uint(fmaf(w, x1, __uint_as_float(o[8 * k + 2 * n + 1])));
                   }
                 }
               }
@@ -490,23 +525,20 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
         tmem_st_wait();
         tc_fence_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.p_full[half]);
+        if (lane == 0) mbar_arrive(&sh.p_full[half][sub]);
       }
-      if (ok) ok = __all_sync(0xffffffffu, wait(&sh.o_full[half], 0));
+      // (one after the other: a parity names a phase only beside the one before it)
+      if (ok) ok = __all_sync(0xffffffffu, wait(&sh.o_done[half], 2 * nt - 2) && wait(&sh.o_done[half], 2 * nt - 1));
       if (ok) {
         tc_fence_after_sync();
-        *mine = l;
-        named_bar_sync(pair_bar, 64);
-        l += *theirs;
         const float w = l != 0.f ? a.v_unit / l : 0.f;
-        // Through the place of q, which no MMA reads any more, so that 8 (D = 64:
-        // 4) lanes write a row's half.
+        // Through the place of q, which no MMA reads any more, so that D / 8
+        // lanes write a row.
         uint8_t *stage = smem + C::Q_OFF + half * C::OPERAND;
 #pragma unroll 1
-        for (int i = side * (D / 2); i < (side + 1) * (D / 2); i += 32) {
+        for (int i = 0; i < D; i += 32) {
           uint32_t o[32];
-          tmem_ld_x32(to + i, o);
-          tmem_ld_wait32(o);
+          tmem_get(to + i, o);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             uint32_t x[4];
@@ -518,8 +550,8 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
           }
         }
         __syncwarp();
-        constexpr int LR = D / 16, PER = 32 / LR;
-        const int piece = side * LR + (lane & (LR - 1));
+        constexpr int LR = D / 8, PER = 32 / LR;
+        const int piece = lane & (LR - 1);
 #pragma unroll 4
         for (int i = 0; i < 32; i += PER) {
           const int rr = (warp & 3) * 32 + i + lane / LR;
@@ -529,8 +561,6 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
         }
         tc_fence_before_sync();
       }
-      // The other warp of these rows may be waiting for this one; it gives up at its next wait.
-      if (!ok) named_bar_arrive(pair_bar, 64);
     }
   } else if (warp == AP_MMA_WARP) {
     // --- the MMAs --------------------------------------------------------------
@@ -540,44 +570,46 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
     // hand over an MMA that runs for 64), with the stages constants.
     const uint64_t q0 = ap_desc_k_major<D>(smem_addr(smem + C::Q_OFF)), k0 = ap_desc_k_major<D>(smem_addr(smem + C::K_OFF)),
                    v0 = ap_desc_n_major<D>(smem_addr(smem + C::V_OFF));
-    constexpr uint32_t ID_S = ap_idesc<Q4>(AP_TILE, false), ID_O = ap_idesc<Q4>(D, true);
+    constexpr uint32_t ID_S = ap_idesc<Q4>(64, false), ID_O = ap_idesc<Q4>(D, true);
     constexpr uint32_t STEP = C::OPERAND >> 4;  // in a descriptor's address units
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
     auto ready = [&](uint64_t *bar, uint32_t parity) { return mbar_try_wait(bar, parity) || wait(bar, parity); };
     // (issued by one elected lane)
-    auto scores = [&](int stage, int half) {
-      const uint64_t q = q0 + half * STEP, k = k0 + stage * STEP;
+    auto scores = [&](int stage, int half, int sub) {  // 64 positions of the stage's K
+      const uint64_t q = q0 + half * STEP, k = k0 + stage * STEP + sub * (STEP / 2);
 #pragma unroll
       for (int ks = 0; ks < D / 16; ++ks) {
         const uint32_t off = (ks >> 2) * (1024 >> 4) + (ks & 3) * 2;
-        mma_bf16_ss(tm + 128 * half, q + off, k + off, ID_S, ks > 0);
+        mma_bf16_ss(tm + 128 * half + 64 * sub, q + off, k + off, ID_S, ks > 0);
       }
-      mma_commit(&sh.s_full[half]);
-      if (half == halves - 1) mma_commit(&sh.k_empty[stage]);
+      mma_commit(&sh.s_full[half][sub]);
+      if (sub == 1 && half == halves - 1) mma_commit(&sh.k_empty[stage]);
     };
     bool ok = ready(&sh.q_full, 0) && ready(&sh.k_full[0], 0);
     tc_fence_after_sync();
     if (ok && elect_lane()) {
-      scores(0, 0);
-      if (halves == 2) scores(0, 1);
+#pragma unroll
+      for (int sub = 0; sub < 2; ++sub) {
+        scores(0, 0, sub);
+        if (halves == 2) scores(0, 1, sub);
+      }
     }
     __syncwarp();
-    // Tile j in stage st: P V, and the scores of the next tile over P.
-    auto half_step = [&](int j, int st, int half, bool skip, bool more) {
-      if (!ready(&sh.p_full[half], st)) return false;
+    // Part sub of tile j in stage st: P V, and the next tile's scores over P.
+    auto part_step = [&](int j, int st, int half, int sub, bool skip, bool more) {
+      if (!ready(&sh.p_full[half][sub], st)) return false;
       tc_fence_after_sync();
       if (elect_lane()) {
         if (!skip) {
-          const uint64_t v = v0 + st * STEP;
+          const uint64_t v = v0 + st * STEP + sub * (STEP / 2);
 #pragma unroll
-          for (int kk = 0; kk < AP_TILE / 16; ++kk)
-            mma_f16_ts(tm + 256 + 128 * half, tm + 128 * half + 8 * kk, v + kk * (2 * C::GROUP >> 4), ID_O, kk > 0 ? 1 : j > 0);
+          for (int kk = 0; kk < 4; ++kk)
+            mma_f16_ts(tm + 256 + 128 * half, tm + 128 * half + 64 * sub + 8 * kk, v + kk * (2 * C::GROUP >> 4), ID_O,
+                       kk > 0 || sub > 0 ? 1 : j > 0);
         }
-        if (half == halves - 1) mma_commit(&sh.v_empty[st]);
-        if (more)
-          scores(st ^ 1, half);
-        else
-          mma_commit(&sh.o_full[half]);
+        mma_commit(&sh.o_done[half]);
+        if (sub == 1 && half == halves - 1) mma_commit(&sh.v_empty[st]);
+        if (more) scores(st ^ 1, half, sub);
       }
       __syncwarp();
       return true;
@@ -587,7 +619,12 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
       const bool more = j + 1 < nt;
       if (!ready(&sh.v_full[st], parity) || (more && !ready(&sh.k_full[st ^ 1], st ? parity ^ 1 : parity))) return false;
       const bool skip = is_odd(st);
-      return half_step(j, st, 0, skip, more) && (halves == 1 || half_step(j, st, 1, skip, more));
+#pragma unroll
+      for (int sub = 0; sub < 2; ++sub) {
+        if (!part_step(j, st, 0, sub, skip, more)) return false;
+        if (halves == 2 && !part_step(j, st, 1, sub, skip, more)) return false;
+      }
+      return true;
     };
     for (int j = 0; j < nt && ok; j += 2) {
       ok = step(j, 0);
@@ -756,12 +793,12 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
       };
       int done = w;  // the warp's first group that is not finished
       bool ok = true;
-      for (int x = w; x < n_groups; x += AP_LOADERS) {
+      for (int x = w; x < n_groups; x += LOADERS) {
         const int j = x >> 3, slot = next;
-        next = slot_of(x + AP_LOADERS);
+        next = slot_of(x + LOADERS);
         if (!room_now(x)) {  // what is on its way is handed over before a wait
           ap_cp_async_wait<0>();
-          for (; done < x; done += AP_LOADERS) finish(done);
+          for (; done < x; done += LOADERS) finish(done);
           ok = room(x);
           if (!ok) break;
         }
@@ -788,23 +825,23 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
           }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
-        if (done <= x - 2 * AP_LOADERS) {  // two groups of this warp stay in flight
+        if (done <= x - 2 * LOADERS) {  // two groups of this warp stay in flight
           ap_cp_async_wait<2>();
           finish(done);
-          done += AP_LOADERS;
+          done += LOADERS;
         }
       }
       ap_cp_async_wait<0>();
       if (ok)
-        for (; done < n_groups; done += AP_LOADERS) finish(done);
+        for (; done < n_groups; done += LOADERS) finish(done);
     } else {
       // Four lanes (D = 128) or two (D = 64) to a position, 16 bytes of codes
       // (32 elements, two scales) each.
       constexpr int CL = D / 32, PER = 32 / CL, NI = 32 / PER;
       const int cl = lane & (CL - 1), t0 = lane / CL;
-      for (int x = w; x < n_groups; x += AP_LOADERS) {
+      for (int x = w; x < n_groups; x += LOADERS) {
         const int j = x >> 3, slot = next;
-        next = slot_of(x + AP_LOADERS);
+        next = slot_of(x + LOADERS);
         const uint8_t *codes = static_cast<const uint8_t *>(x & 4 ? a.v : a.k) + cl * 16;
         const uint8_t *scales = (x & 4 ? a.vs : a.ks) + cl * 2;
         uint4 q[NI];
@@ -905,7 +942,7 @@ static cudaError_t launch_prompt(const ApArgs &p, const CUtensorMap &k_map, cons
     if (dev < 64) done[dev] = 1;
   }
   const long long grid = (long long)p.n_rt * p.a.H * p.a.B;
-  return launch_pdl(attn_prompt_kernel<MODE, D>, dim3((unsigned)grid), dim3(AP_THREADS), smem, s, p, k_map, v_map);
+  return launch_pdl(attn_prompt_kernel<MODE, D>, dim3((unsigned)grid), dim3(ap_threads(MODE)), smem, s, p, k_map, v_map);
 }
 
 cudaError_t launch_attn_prompt(const AttnArgs &a, bool q4, cudaStream_t s) {

@@ -394,3 +394,16 @@ def test_no_rows(q4):
     ml = needs_gpu()
     c = Case(q4, [5], 1, 4, 2, 128, 16).device()
     assert c.call(ml, y=c.y_d[:0]).shape == (0, 512)
+
+
+@both
+def test_windowed_prompts_have_the_same_bits_every_time(q4):
+    """Few sink tokens set a row's maximum before its window raises it: the
+    outputs are rescaled while products are on their way."""
+    ml = needs_gpu()
+    c = Case(q4, [127, 1, 300], 129, 5, 1, 128, 32, seed=129)
+    out, _ = c.check(ml, window=100, sinks=5)
+    ws = ml.Workspace(ml.attention_workspace_bytes(3 * 129, 129, 5, 1, 128))
+    for _ in range(50):
+        assert torch.equal(c.call(ml, window=100, sinks=5, ws=ws), out)
+    assert ws.status() == 0
