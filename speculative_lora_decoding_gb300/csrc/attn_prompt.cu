@@ -16,10 +16,12 @@
 // in tensor memory) only when a score exceeds it by 8 in log2 units; until
 // then a tile is one pass over its scores.
 //
-// Warps 0-3 and 4-7 hold the rows of the two halves, warp 8 issues the MMAs, the
+// Warps 0-3 and 4-7 hold the rows of the two halves, warps 8 and 9 issue their
+// MMAs (an MMA is handed over as the one before it runs, so a warp's waits would
+// leave the tensor cores idle; with two, one waits while the other issues), the
 // others bring the tiles into 128-byte-swizzled rows (K read K-major, V
 // along its rows), in one of three ways:
-//   boxes   bf16 cache whose pages are multiples of 8 positions: warp 9 copies
+//   boxes   bf16 cache whose pages are multiples of 8 positions: warp 10 copies
 //           boxes of a page's positions by TMA, a lane to a box;
 //   pieces  other pages: a gather of 16-byte pieces;
 //   codes   4-bit cache: codes are expanded to fp16 on the way, exactly.
@@ -51,12 +53,12 @@ struct ApCfg {
 };
 
 enum { AP_BOXES = 0, AP_PIECES = 1, AP_CODES = 2 };
-// Warps that bring tiles: with boxes one copies and two look the tiles over.
-__host__ __device__ constexpr int ap_loaders(int mode) { return mode == AP_BOXES ? 3 : 7; }
-__host__ __device__ constexpr int ap_threads(int mode) { return 32 * (AP_MMA_WARP + 1 + ap_loaders(mode)); }
+// Warps that bring tiles: with boxes one copies and one looks the tiles over.
+__host__ __device__ constexpr int ap_loaders(int mode) { return mode == AP_BOXES ? 2 : 6; }
+__host__ __device__ constexpr int ap_threads(int mode) { return 32 * (AP_MMA_WARP + 2 + ap_loaders(mode)); }
 
 struct __align__(16) ApShared {
-  uint64_t q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], v_land[2], s_full[2][2], p_full[2][2], o_done[2], fin;
+  uint64_t q_full, k_full[2], v_full[2], v_land[2], kv_empty[2], k0_empty, s_full[2][2], p_full[2][2], fin[2];
   uint32_t tmem;
   int abort;
   alignas(16) uint32_t there[4][AP_GROUPS];  // of the last tiles: positions whose slot is in the cache
@@ -301,18 +303,17 @@ __global__ void __launch_bounds__(ap_threads(MODE), 1)
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.k_full[i], MODE == AP_BOXES ? 1 : AP_GROUPS);
-      mbar_init(&sh.v_full[i], MODE == AP_BOXES ? 2 : AP_GROUPS);
+      mbar_init(&sh.v_full[i], MODE == AP_BOXES ? 1 : AP_GROUPS);
       mbar_init(&sh.v_land[i], 1);
-      mbar_init(&sh.k_empty[i], 1);
-      mbar_init(&sh.v_empty[i], 1);
+      mbar_init(&sh.kv_empty[i], halves);
+      mbar_init(&sh.fin[i], 1);
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         mbar_init(&sh.s_full[i][k], 1);
         mbar_init(&sh.p_full[i][k], 4);
       }
-      mbar_init(&sh.o_done[i], 1);
     }
-    mbar_init(&sh.fin, 1);
+    mbar_init(&sh.k0_empty, halves);
 #pragma unroll
     for (int i = 0; i < 2 * AP_GROUPS; ++i) (&sh.odd[0][0])[i] = 0;
     sh.abort = 0;
@@ -343,6 +344,10 @@ __global__ void __launch_bounds__(ap_threads(MODE), 1)
     const int j0 = attn_tile_start<AP_TILE>(R, j), jl = j0 + AP_TILE - 1;
     return jl > p_lo || (a.window && !(j0 > p_hi - a.window || jl < a.sinks));
   };
+  // What says that the stage of K or V of tile j >= 2 is free: V of tile j - 2 is
+  // freed with K of the tile after it.
+  auto empty_bar = [&](int j, bool v) { return v ? &sh.kv_empty[j & 1] : j == 2 ? &sh.k0_empty : &sh.kv_empty[(j - 3) & 1]; };
+  auto empty_phase = [&](int j, bool v) { return v ? (j - 2) >> 1 : j == 2 ? 0 : (j - 3) >> 1; };
   auto is_odd = [&](int stage) {  // (V of the stage's tile has landed)
     const int4 f = *reinterpret_cast<const int4 *>(sh.odd[stage]);
     return (f.x | f.y | f.z | f.w) != 0;
@@ -454,10 +459,10 @@ __global__ void __launch_bounds__(ap_threads(MODE), 1)
         const float d = fmaf(mx, mul, -base);
         const bool far = mx > AP_NONE && (d > AP_SLACK || m == AP_NONE);
         const bool any_far = __any_sync(0xffffffffu, far);
-        // O is about to be touched: the product before must be done (the one
-        // before that is, since these scores came after it).
+        // O is about to be touched: the product before must be done, after which
+        // the next part's scores are signalled.
         if ((any_far || odd) && i > 0) {
-          ok = __all_sync(0xffffffffu, wait(&sh.o_done[half], i - 1));
+          ok = __all_sync(0xffffffffu, wait(&sh.s_full[half][sub ^ 1], (i + 1) >> 1));
           if (!ok) break;
           tc_fence_after_sync();
         }
@@ -527,8 +532,8 @@ __global__ void __launch_bounds__(ap_threads(MODE), 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.p_full[half][sub]);
       }
-      // (one after the other: a parity names a phase only beside the one before it)
-      if (ok) ok = __all_sync(0xffffffffu, wait(&sh.o_done[half], 2 * nt - 2) && wait(&sh.o_done[half], 2 * nt - 1));
+      // (past the last tile the scores' barriers stand for the products alone)
+      if (ok) ok = __all_sync(0xffffffffu, wait(&sh.s_full[half][0], nt) && wait(&sh.s_full[half][1], nt));
       if (ok) {
         tc_fence_after_sync();
         const float w = l != 0.f ? a.v_unit / l : 0.f;
@@ -562,82 +567,78 @@ __global__ void __launch_bounds__(ap_threads(MODE), 1)
         tc_fence_before_sync();
       }
     }
-  } else if (warp == AP_MMA_WARP) {
-    // --- the MMAs --------------------------------------------------------------
-    // What this warp spends between a barrier's completion and the next MMA is
-    // time in which the tensor cores wait: the whole warp runs the loop, on
-    // values that are the same in all lanes (one lane alone took 70 cycles to
-    // hand over an MMA that runs for 64), with the stages constants.
-    const uint64_t q0 = ap_desc_k_major<D>(smem_addr(smem + C::Q_OFF)), k0 = ap_desc_k_major<D>(smem_addr(smem + C::K_OFF)),
-                   v0 = ap_desc_n_major<D>(smem_addr(smem + C::V_OFF));
-    constexpr uint32_t ID_S = ap_idesc<Q4>(64, false), ID_O = ap_idesc<Q4>(D, true);
-    constexpr uint32_t STEP = C::OPERAND >> 4;  // in a descriptor's address units
-    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-    auto ready = [&](uint64_t *bar, uint32_t parity) { return mbar_try_wait(bar, parity) || wait(bar, parity); };
-    // (issued by one elected lane)
-    auto scores = [&](int stage, int half, int sub) {  // 64 positions of the stage's K
-      const uint64_t q = q0 + half * STEP, k = k0 + stage * STEP + sub * (STEP / 2);
+  } else if (warp < AP_MMA_WARP + 2) {
+    const int half = warp - AP_MMA_WARP;
+    if (half < halves) {
+      // --- a half's MMAs --------------------------------------------------------
+      // The whole warp runs the loop, on values that are the same in all lanes
+      // (one lane alone took 70 cycles to hand over an MMA that runs for 64),
+      // with the stages constants.
+      constexpr uint32_t ID_S = ap_idesc<Q4>(64, false), ID_O = ap_idesc<Q4>(D, true);
+      constexpr uint32_t STEP = C::OPERAND >> 4;  // in a descriptor's address units
+      const uint64_t q0 = ap_desc_k_major<D>(smem_addr(smem + C::Q_OFF)) + half * STEP,
+                     k0 = ap_desc_k_major<D>(smem_addr(smem + C::K_OFF)), v0 = ap_desc_n_major<D>(smem_addr(smem + C::V_OFF));
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0), ts = tm + 128 * half, to = tm + 256 + 128 * half;
+      auto ready = [&](uint64_t *bar, uint32_t parity) { return mbar_try_wait(bar, parity) || wait(bar, parity); };
+      // (issued by one elected lane)
+      auto scores = [&](int stage, int sub) {  // 64 positions of the stage's K
+        const uint64_t k = k0 + stage * STEP + sub * (STEP / 2);
 #pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks) {
-        const uint32_t off = (ks >> 2) * (1024 >> 4) + (ks & 3) * 2;
-        mma_bf16_ss(tm + 128 * half + 64 * sub, q + off, k + off, ID_S, ks > 0);
-      }
-      mma_commit(&sh.s_full[half][sub]);
-      if (sub == 1 && half == halves - 1) mma_commit(&sh.k_empty[stage]);
-    };
-    bool ok = ready(&sh.q_full, 0) && ready(&sh.k_full[0], 0);
-    tc_fence_after_sync();
-    if (ok && elect_lane()) {
-#pragma unroll
-      for (int sub = 0; sub < 2; ++sub) {
-        scores(0, 0, sub);
-        if (halves == 2) scores(0, 1, sub);
-      }
-    }
-    __syncwarp();
-    // Part sub of tile j in stage st: P V, and the next tile's scores over P.
-    auto part_step = [&](int j, int st, int half, int sub, bool skip, bool more) {
-      if (!ready(&sh.p_full[half][sub], st)) return false;
-      tc_fence_after_sync();
-      if (elect_lane()) {
-        if (!skip) {
-          const uint64_t v = v0 + st * STEP + sub * (STEP / 2);
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_f16_ts(tm + 256 + 128 * half, tm + 128 * half + 64 * sub + 8 * kk, v + kk * (2 * C::GROUP >> 4), ID_O,
-                       kk > 0 || sub > 0 ? 1 : j > 0);
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const uint32_t off = (ks >> 2) * (1024 >> 4) + (ks & 3) * 2;
+          mma_bf16_ss(ts + 64 * sub, q0 + off, k + off, ID_S, ks > 0);
         }
-        mma_commit(&sh.o_done[half]);
-        if (sub == 1 && half == halves - 1) mma_commit(&sh.v_empty[st]);
-        if (more) scores(st ^ 1, half, sub);
-      }
-      __syncwarp();
-      return true;
-    };
-    auto step = [&](int j, int st) {
-      const uint32_t parity = (j >> 1) & 1;
-      const bool more = j + 1 < nt;
-      if (!ready(&sh.v_full[st], parity) || (more && !ready(&sh.k_full[st ^ 1], st ? parity ^ 1 : parity))) return false;
-      const bool skip = is_odd(st);
+      };
+      bool ok = ready(&sh.q_full, 0) && ready(&sh.k_full[0], 0);
+      tc_fence_after_sync();
+      if (ok && elect_lane()) {
 #pragma unroll
-      for (int sub = 0; sub < 2; ++sub) {
-        if (!part_step(j, st, 0, sub, skip, more)) return false;
-        if (halves == 2 && !part_step(j, st, 1, sub, skip, more)) return false;
+        for (int sub = 0; sub < 2; ++sub) {
+          scores(0, sub);
+          mma_commit(&sh.s_full[half][sub]);
+        }
+        mma_commit(&sh.k0_empty);
       }
-      return true;
-    };
-    for (int j = 0; j < nt && ok; j += 2) {
-      ok = step(j, 0);
-      if (ok && j + 1 < nt) ok = step(j + 1, 1);
-    }
-    if (!ok) {  // what was issued ends before the tensor memory goes back
-      int never = 0;
-      if (elect_lane()) mma_commit(&sh.fin);
       __syncwarp();
-      mbar_wait_bounded(&sh.fin, 0, &never);
+      // Part sub of tile j in stage st: P V, and the next tile's scores over P.
+      // One commit stands for both; one frees V of tile j and K of tile j + 1.
+      auto part_step = [&](int j, int st, int sub, bool skip, bool more) {
+        if (!ready(&sh.p_full[half][sub], st)) return false;
+        tc_fence_after_sync();
+        if (elect_lane()) {
+          if (!skip) {
+            const uint64_t v = v0 + st * STEP + sub * (STEP / 2);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              mma_f16_ts(to, ts + 64 * sub + 8 * kk, v + kk * (2 * C::GROUP >> 4), ID_O, kk > 0 || sub > 0 ? 1 : j > 0);
+          }
+          if (more) scores(st ^ 1, sub);
+          mma_commit(&sh.s_full[half][sub]);
+          if (sub == 1) mma_commit(&sh.kv_empty[st]);
+        }
+        __syncwarp();
+        return true;
+      };
+      auto step = [&](int j, int st) {
+        const bool more = j + 1 < nt;
+        const uint32_t parity = (j >> 1) & 1;
+        if (!ready(&sh.v_full[st], parity) || (more && !ready(&sh.k_full[st ^ 1], st ? parity ^ 1 : parity))) return false;
+        const bool skip = is_odd(st);
+        return part_step(j, st, 0, skip, more) && part_step(j, st, 1, skip, more);
+      };
+      for (int j = 0; j < nt && ok; j += 2) {
+        ok = step(j, 0);
+        if (ok && j + 1 < nt) ok = step(j + 1, 1);
+      }
+      if (!ok) {  // what was issued ends before the tensor memory goes back
+        int never = 0;
+        if (elect_lane()) mma_commit(&sh.fin[half]);
+        __syncwarp();
+        mbar_wait_bounded(&sh.fin[half], 0, &never);
+      }
     }
   } else if (MODE == AP_BOXES) {
-    if (warp == AP_MMA_WARP + 1) {
+    if (warp == AP_MMA_WARP + 2) {
       // --- the tiles, by TMA: lane i brings the tile's box i ---------------------
       const int lb = p.box_log2, n_box = AP_TILE >> lb, bytes = (128 * (D / 64)) << lb;
       auto slot_of = [&](int j) {  // the box's first slot; -1: none
@@ -664,7 +665,7 @@ __global__ void __launch_bounds__(ap_threads(MODE), 1)
         const uint32_t all = n_box == 32 ? 0xffffffffu : (1u << n_box) - 1u;
 #pragma unroll
         for (int v = 0; v < 2; ++v) {
-          ok = j < 2 || __all_sync(0xffffffffu, wait(v ? &sh.v_empty[j & 1] : &sh.k_empty[j & 1], (j >> 1) - 1));
+          ok = j < 2 || __all_sync(0xffffffffu, wait(empty_bar(j, v), empty_phase(j, v)));
           if (!ok) break;
           uint8_t *dst = smem + (v ? C::V_OFF : C::K_OFF) + (j & 1) * C::OPERAND;
           if (there != all) {  // boxes that are not read are zeros
@@ -695,10 +696,10 @@ __global__ void __launch_bounds__(ap_threads(MODE), 1)
             last_bar[v][0] = bar;
             last_parity[v][0] = parity & 1u;
           }
-          if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(__popc(there) * bytes));
-          if (lane < 2 && v && !land) sh.odd[j & 1][lane] = 0;
-          __syncwarp();
-          if (lane == 1 && v && !land) mbar_arrive(bar);  // (for the two warps that look tiles over)
+          if (lane == 0) {
+            if (v && !land) sh.odd[j & 1][0] = 0;
+            mbar_arrive_expect_tx(bar, (uint32_t)(__popc(there) * bytes));
+          }
           __syncwarp();
           if (slot >= 0)
             tma_load_5d(dst + ((lane << lb) >> 3) * C::GROUP, v ? &v_map : &k_map, bar, 0, 0, 0, slot >> 3, h, policy);
@@ -719,9 +720,8 @@ __global__ void __launch_bounds__(ap_threads(MODE), 1)
         if (!__all_sync(0xffffffffu, wait(&sh.v_land[st], st ? uses[1]++ : uses[0]++))) break;
         bool odd = false;
         const uint4 *v = reinterpret_cast<const uint4 *>(smem + C::V_OFF + st * C::OPERAND);
-        const int who = warp - AP_MMA_WARP - 2;
 #pragma unroll 8
-        for (int i = 32 * who + lane; i < C::OPERAND / 16; i += 64) {
+        for (int i = lane; i < C::OPERAND / 16; i += 32) {
           const uint4 q = v[i];
           const uint32_t e[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
@@ -729,7 +729,7 @@ __global__ void __launch_bounds__(ap_threads(MODE), 1)
         }
         odd = __any_sync(0xffffffffu, odd);
         if (lane == 0) {
-          sh.odd[st][who] = odd;
+          sh.odd[st][0] = odd;
           mbar_arrive(&sh.v_full[st]);
         }
         __syncwarp();
@@ -754,19 +754,19 @@ __global__ void __launch_bounds__(ap_threads(MODE), 1)
     };
     auto room = [&](int x) {  // wait until the half-tile's place is free
       const int j = x >> 3;
-      return j < 2 || __all_sync(0xffffffffu, wait(x & 4 ? &sh.v_empty[j & 1] : &sh.k_empty[j & 1], (j >> 1) - 1));
+      return j < 2 || __all_sync(0xffffffffu, wait(empty_bar(j, x & 4), empty_phase(j, x & 4)));
     };
     auto room_now = [&](int x) {
       const int j = x >> 3;
       return j < 2 ||
-             __all_sync(0xffffffffu, mbar_test(x & 4 ? &sh.v_empty[j & 1] : &sh.k_empty[j & 1], ((j >> 1) - 1) & 1));
+             __all_sync(0xffffffffu, mbar_test(empty_bar(j, x & 4), empty_phase(j, x & 4) & 1));
     };
     auto arrive = [&](int x) {  // this warp's part of it is there
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(x & 4 ? &sh.v_full[(x >> 3) & 1] : &sh.k_full[(x >> 3) & 1]);
     };
-    const int w = warp - AP_MMA_WARP - 1;
+    const int w = warp - AP_MMA_WARP - 2;
     int next = slot_of(w);
     if (!Q4) {
       constexpr int CH = D / 8, PER = 32 / CH;  // 16-byte pieces of a row, rows per instruction
