@@ -340,9 +340,11 @@ __global__ void __launch_bounds__(ap_threads(MODE), 1)
   // P over each, O at 256 + 128 i.
 
   // Whether some row of the CTA does not see all of tile j.
+  const int all_below = (int)min(p_lo, 0x7ffffff0ll);  // every row sees up to here, but for its window's start
+  const int all_above = a.window ? (int)min(max(p_hi - a.window, -1ll), 0x7ffffff0ll) : -1;
   auto partial = [&](int j) {
     const int j0 = attn_tile_start<AP_TILE>(R, j), jl = j0 + AP_TILE - 1;
-    return jl > p_lo || (a.window && !(j0 > p_hi - a.window || jl < a.sinks));
+    return jl > all_below || (j0 <= all_above && jl >= a.sinks);
   };
   // What says that the stage of K or V of tile j >= 2 is free: V of tile j - 2 is
   // freed with K of the tile after it.
@@ -423,19 +425,17 @@ __global__ void __launch_bounds__(ap_threads(MODE), 1)
       for (int i = 0; i < 2 * nt; ++i) {  // part i & 1 of tile i / 2
         const int j = i >> 1, sub = i & 1;
         const bool part = partial(j);
-        ok = wait(&sh.s_full[half][sub], j) && (!part || wait(&sh.v_full[j & 1], j >> 1));
-        if (!__all_sync(0xffffffffu, ok)) {
-          ok = false;
-          break;
-        }
+        if (!__all_sync(0xffffffffu, mbar_try_wait(&sh.s_full[half][sub], j & 1)))
+          ok = __all_sync(0xffffffffu, wait(&sh.s_full[half][sub], j));
+        if (ok && part) ok = __all_sync(0xffffffffu, wait(&sh.v_full[j & 1], j >> 1));
+        if (!ok) break;
         tc_fence_after_sync();
         if (Q4 && i == 0) mul *= q_exp[row];  // (the scores of all rows are there, so their q was)
         const int j0 = attn_tile_start<AP_TILE>(R, j) + 64 * sub, jl = j0 + 63;
         const uint32_t sc = ts + 64 * sub;
         const uint32_t *there = sh.there[j & 3] + 2 * sub;
         const bool odd = part && is_odd(j & 1);
-        const bool edge = (there[0] & there[1]) != 0xffffffffu || jl > hi_first ||
-                          (a.window && !(j0 > lo_last || jl < a.sinks));
+        const bool edge = (there[0] & there[1]) != 0xffffffffu || jl > hi_first || (j0 <= lo_last && jl >= a.sinks);
         // The positions 32 ch .. 32 ch + 31 of the part that this row sees, as bits.
         auto seen = [&](int ch) {
           auto below = [](int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u; };
