@@ -7,9 +7,14 @@
 //   scale = E4M3(amax / (6 unit)),   code = E2M1(v / (scale unit)),
 // fp32 with IEEE division, so that the codes follow from the inputs alone.
 //
-// Both kernels are copies that change the format: one thread per (row, K or V,
-// head, group), 32 bytes of bf16 on one side and 8 + 1 bytes on the other, all
-// of them contiguous across a warp within a head.
+// Both kernels are copies that change the format and are bound by HBM: a row
+// of the pass (a position, with all heads of K and V) per slice of threads, a
+// thread per group of 16: 32 bytes of bf16 on one side and 8 + 1 bytes on the
+// other.  What a thread's group fixes (K or V, head, place in the row) stays
+// the same from row to row, and a row's slot and values are asked for a row ahead.
+#include <climits>
+#include <cmath>
+
 #include "common.cuh"
 #include "e2m1.cuh"
 #include "launch.h"
@@ -20,137 +25,212 @@ constexpr int KV4_THREADS = 256;
 
 // The slot (block, offset) of a position through a request's table as the
 // index of head 0's row, (block * H) * block_size + offset; -1 outside.
-__device__ __forceinline__ long long kv4_slot(const Kv4 &c, int b, long long pos) {
-  const long long j = pos / c.block_size;
-  const int blk = pos >= 0 && j < c.max_blocks ? c.block_table[(size_t)b * c.max_blocks + j] : -1;
+__device__ __forceinline__ int kv4_slot(const Kv4 &c, int b, long long pos) {
+  const long long j = pos >= 0 && pos <= INT32_MAX ? (long long)((uint32_t)pos / (uint32_t)c.block_size) : c.max_blocks;
+  const int blk = j < c.max_blocks ? __ldg(c.block_table + (size_t)b * c.max_blocks + j) : -1;
   if (blk < 0 || blk >= c.num_blocks) return -1;
-  return (long long)blk * c.H * c.block_size + (pos - j * c.block_size);
+  return blk * c.H * c.block_size + (int)(pos - j * c.block_size);
 }
 
-// VEC: every row of y starts on a 16-byte boundary.
-template <bool VEC>
-__global__ void __launch_bounds__(KV4_THREADS) kv_write_q4_kernel(const Kv4Write a) {
+// v / s for the codes.  EXACT: IEEE division.  Otherwise the unit is a power
+// of two, v has 8 significant bits, s 4 and a border between two codes 3, so
+// a quotient that is not on a border is at least 2^-8 of it away: v (1 / s),
+// within 2^-22 of the quotient, rounded to 12 bits falls on the same side, or
+// on the border itself.
+template <bool EXACT>
+__device__ __forceinline__ float kv4_ratio(float v, float s, float r) {
+  if (EXACT) return __fdiv_rn(v, s);
+  return __uint_as_float((__float_as_uint(v * r) + 0x800u) & 0xFFFFF000u);
+}
+
+// 32 bytes in one access (32-byte aligned).
+__device__ __forceinline__ void ldg_32(const void *p, uint32_t (&w)[8]) {
+  asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+               : "l"(p));
+}
+__device__ __forceinline__ void stg_32(void *p, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
+// Slices of `lanes` threads, each with a row at a time.  VEC: every row of y
+// starts on a 32-byte boundary.
+template <bool VEC, bool EXACT>
+__global__ void __launch_bounds__(KV4_THREADS) kv_write_q4_kernel(const Kv4Write a, int lanes) {
   grid_launch_dependents();
   grid_dependency_wait();  // y comes from the projection just before
-  const int GD = a.c.D / Q4_GROUP;
-  const int per_row = 2 * a.c.H * GD;
-  const long long n = (long long)a.M * per_row;
-  for (long long i = (long long)blockIdx.x * KV4_THREADS + threadIdx.x; i < n; i += (long long)gridDim.x * KV4_THREADS) {
-    const int m = (int)(i / per_row);
-    int r = (int)(i - (long long)m * per_row);
-    const int kv = r >= a.c.H * GD;
-    r -= kv * a.c.H * GD;
-    const int h = r / GD, g = r - h * GD;
+  const int GD = a.c.D / Q4_GROUP, per = a.c.H * GD;
+  const int slices = KV4_THREADS / lanes, slice = threadIdx.x / lanes, lane = threadIdx.x - slice * lanes;
+  const int stride = gridDim.x * slices;
+  auto slot_of = [&](int m) {
+    if (m >= a.M) return -1;
     const int b = m / a.rows_per_req, t = m - b * a.rows_per_req;
-    const int L = a.seq_len[b];
-    if (L < 0) continue;  // unused request slot
-    const long long slot = kv4_slot(a.c, b, (long long)L + a.t0 + t);
-    if (slot < 0) {
-      raise_status(a.c.status, MLORA_DEV_BAD_SLOT);
-      continue;
-    }
-    const uint16_t *src = a.y + (size_t)m * a.ld + a.col[kv] + h * a.c.D + g * Q4_GROUP;
-    uint32_t w[8];
-    if (VEC) {
-      const uint4 v0 = __ldg(reinterpret_cast<const uint4 *>(src));
-      const uint4 v1 = __ldg(reinterpret_cast<const uint4 *>(src) + 1);
-      w[0] = v0.x; w[1] = v0.y; w[2] = v0.z; w[3] = v0.w;
-      w[4] = v1.x; w[5] = v1.y; w[6] = v1.z; w[7] = v1.w;
-    } else {
+    const int L = __ldg(a.seq_len + b);
+    if (L < 0) return -1;  // unused request slot
+    const int slot = kv4_slot(a.c, b, (long long)L + a.t0 + t);
+    if (slot < 0 && lane == 0) raise_status(a.c.status, MLORA_DEV_BAD_SLOT);
+    return slot;
+  };
+  for (int i = lane; i < 2 * per; i += lanes) {
+    const int kv = i >= per, e = i - (kv ? per : 0), h = e / GD, g = e - h * GD;
+    const float unit = a.c.unit[kv], unit6 = 6.f * unit;
+    const uint16_t *const y = a.y + a.col[kv] + e * Q4_GROUP;
+    uint8_t *const codes = a.c.codes[kv] + (size_t)h * a.c.block_size * (a.c.D / 2) + g * 8;
+    uint8_t *const scales = a.c.scales[kv] + (size_t)h * a.c.block_size * GD + g;
+    int m = blockIdx.x * slices + slice, next = slot_of(m);
+    auto fetch = [&](int row, uint32_t (&w)[8]) {
+      if (row >= a.M) return;
+      const uint16_t *src = y + (size_t)row * a.ld;
+      if (VEC) {
+        ldg_32(src, w);
+      } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) w[e] = (uint32_t)src[2 * e] | ((uint32_t)src[2 * e + 1] << 16);
-    }
-    // The largest magnitude by its bits: a NaN's lie above every number's, so
-    // a NaN anywhere in the group reaches the scale.
-    uint32_t mx = 0;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) mx = max(mx, max(w[e] & 0x7FFFu, (w[e] >> 16) & 0x7FFFu));
-    const float unit = a.c.unit[kv];
-    const uint32_t sc = cvt_e4m3(__fdiv_rn(__uint_as_float(mx << 16), 6.f * unit));
-    const float s = e4m3_to_float(sc) * unit;
-    uint2 codes = make_uint2(0u, 0u);
-    if (s != 0.f) {
-      float v[8];
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          v[2 * e] = __fdiv_rn(__uint_as_float(w[4 * half + e] << 16), s);
-          v[2 * e + 1] = __fdiv_rn(__uint_as_float(w[4 * half + e] & 0xFFFF0000u), s);
-        }
-        (half ? codes.y : codes.x) = cvt_e2m1x8(v);
+        for (int k = 0; k < 8; ++k) w[k] = (uint32_t)src[2 * k] | ((uint32_t)src[2 * k + 1] << 16);
       }
+    };
+    uint32_t ahead[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    fetch(m, ahead);
+    for (; m < a.M; m += stride) {
+      uint32_t w[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) w[k] = ahead[k];
+      fetch(m + stride, ahead);
+      const int slot = next;
+      next = slot_of(m + stride);
+      if (slot < 0) continue;
+      // The largest magnitude by its bits: a NaN's lie above every number's, so
+      // a NaN anywhere in the group reaches the scale.
+      uint32_t mx = 0;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) mx = max(mx, max(w[k] & 0x7FFFu, (w[k] >> 16) & 0x7FFFu));
+      const uint32_t sc = cvt_e4m3(__fdiv_rn(__uint_as_float(mx << 16), unit6));
+      const float s = e4m3_to_float(sc) * unit, r = EXACT ? 0.f : __fdiv_rn(1.f, s);
+      uint2 c = make_uint2(0u, 0u);
+      if (s != 0.f) {
+        float v[8];
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            v[2 * k] = kv4_ratio<EXACT>(__uint_as_float(w[4 * half + k] << 16), s, r);
+            v[2 * k + 1] = kv4_ratio<EXACT>(__uint_as_float(w[4 * half + k] & 0xFFFF0000u), s, r);
+          }
+          (half ? c.y : c.x) = cvt_e2m1x8(v);
+        }
+      }
+      *reinterpret_cast<uint2 *>(codes + (size_t)slot * (a.c.D / 2)) = c;
+      scales[(size_t)slot * GD] = (uint8_t)sc;
     }
-    const size_t row = (size_t)(slot + (long long)h * a.c.block_size);
-    *reinterpret_cast<uint2 *>(a.c.codes[kv] + row * (a.c.D / 2) + g * 8) = codes;
-    a.c.scales[kv][row * GD + g] = (uint8_t)sc;
   }
 }
 
-__global__ void __launch_bounds__(KV4_THREADS) kv_read_q4_kernel(const Kv4Read a) {
+template <bool VEC>
+__global__ void __launch_bounds__(KV4_THREADS) kv_read_q4_kernel(const Kv4Read a, int lanes) {
   grid_launch_dependents();
   grid_dependency_wait();  // the cache may come from the write just before
-  const int GD = a.c.D / Q4_GROUP;
-  const int per_row = a.c.H * GD;
-  const long long per = (long long)a.c.B * a.rows * per_row, n = 2 * per;
-  for (long long i = (long long)blockIdx.x * KV4_THREADS + threadIdx.x; i < n; i += (long long)gridDim.x * KV4_THREADS) {
-    const int kv = i >= per;
-    const long long o = i - (kv ? per : 0);
-    const int m = (int)(o / per_row);
-    const int r = (int)(o - (long long)m * per_row);
-    const int h = r / GD, g = r - h * GD;
-    const int b = m / a.rows, t = m - b * a.rows;
-    const int L = a.start[b];
+  const int GD = a.c.D / Q4_GROUP, per = a.c.H * GD, M = a.c.B * a.rows;
+  const int slices = KV4_THREADS / lanes, slice = threadIdx.x / lanes, lane = threadIdx.x - slice * lanes;
+  const long long stride = (long long)gridDim.x * slices;
+  auto slot_of = [&](long long m) {
+    if (m >= M) return -1;
+    const int b = (int)m / a.rows, t = (int)m - b * a.rows;
+    const int L = __ldg(a.start + b);
     const long long pos = (long long)L + t;
-    uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
-    if (L >= 0 && pos < a.end[b]) {
-      const long long slot = kv4_slot(a.c, b, pos);
-      if (slot < 0) {
-        raise_status(a.c.status, MLORA_DEV_BAD_SLOT);
-      } else {
-        const size_t row = (size_t)(slot + (long long)h * a.c.block_size);
-        const uint2 codes = __ldg(reinterpret_cast<const uint2 *>(a.c.codes[kv] + row * (a.c.D / 2) + g * 8));
-        const float s = e4m3_to_float(__ldg(a.c.scales[kv] + row * GD + g));
-        const float unit = a.c.unit[kv];
-        uint32_t w[8];
+    if (L < 0 || pos >= __ldg(a.end + b)) return -1;
+    const int slot = kv4_slot(a.c, b, pos);
+    if (slot < 0 && lane == 0) raise_status(a.c.status, MLORA_DEV_BAD_SLOT);
+    return slot;
+  };
+  for (int i = lane; i < 2 * per; i += lanes) {
+    const int kv = i >= per, e = i - (kv ? per : 0), h = e / GD, g = e - h * GD;
+    const float unit = a.c.unit[kv];
+    const uint8_t *const codes = a.c.codes[kv] + (size_t)h * a.c.block_size * (a.c.D / 2) + g * 8;
+    const uint8_t *const scales = a.c.scales[kv] + (size_t)h * a.c.block_size * GD + g;
+    // Two rows ahead: a row's codes are asked for while the row before is written.
+    long long m = (long long)blockIdx.x * slices + slice;
+    int next = slot_of(m), after = slot_of(m + stride);
+    uint2 c1 = make_uint2(0, 0);
+    uint32_t s1 = 0;
+    auto ask = [&](int slot) {
+      c1 = make_uint2(0, 0);
+      s1 = 0;
+      if (slot >= 0) {
+        c1 = __ldg(reinterpret_cast<const uint2 *>(codes + (size_t)slot * (a.c.D / 2)));
+        s1 = __ldg(scales + (size_t)slot * GD);
+      }
+    };
+    ask(next);
+    for (; m < M; m += stride) {
+      const int slot = next;
+      const uint2 c = c1;
+      const uint32_t sc = s1;
+      next = after;
+      ask(next);
+      after = slot_of(m + 2 * stride);
+      uint32_t w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+      if (slot >= 0) {
+        const float s = e4m3_to_float(sc);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           uint32_t f[4];
-          e2m1x8_to_f16(half ? codes.y : codes.x, f);
+          e2m1x8_to_f16(half ? c.y : c.x, f);
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
+          for (int k = 0; k < 4; ++k)
             // code * scale is exact; the product with unit is rounded to fp32
             // (exact for a power of two), then once to bf16.
-            w[4 * half + e] = (uint32_t)float_to_bf16_bits(f16_lo(f[e]) * s * unit) |
-                              ((uint32_t)float_to_bf16_bits(f16_hi(f[e]) * s * unit) << 16);
+            w[4 * half + k] = (uint32_t)float_to_bf16_bits(f16_lo(f[k]) * s * unit) |
+                              ((uint32_t)float_to_bf16_bits(f16_hi(f[k]) * s * unit) << 16);
         }
-        lo = make_uint4(w[0], w[1], w[2], w[3]);
-        hi = make_uint4(w[4], w[5], w[6], w[7]);
+      }
+      uint4 *dst = reinterpret_cast<uint4 *>(a.out[kv] + ((size_t)m * per + e) * Q4_GROUP);
+      if (VEC) {
+        stg_32(dst, w);
+      } else {
+        dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
       }
     }
-    uint4 *dst = reinterpret_cast<uint4 *>(a.out[kv] + (size_t)o * Q4_GROUP);
-    dst[0] = lo;
-    dst[1] = hi;
   }
 }
 
-static unsigned kv4_grid(long long n, int num_sms) {
-  const long long want = (n + KV4_THREADS - 1) / KV4_THREADS, cap = (long long)num_sms * 8;
+// Threads to a row: a power of two, as many as its groups, 32 at least.
+static int kv4_lanes(const Kv4 &c) {
+  int lanes = 32;
+  while (lanes < KV4_THREADS && lanes < 2 * c.H * (c.D / Q4_GROUP)) lanes *= 2;
+  return lanes;
+}
+
+static unsigned kv4_grid(long long rows, int lanes, int num_sms) {
+  const long long slices = KV4_THREADS / lanes, want = (rows + slices - 1) / slices, cap = (long long)num_sms * 8;
   return (unsigned)(want < cap ? want : cap);
 }
 
 cudaError_t launch_kv_write_q4(const Kv4Write &a, int num_sms, cudaStream_t s) {
   if (a.M <= 0) return cudaSuccess;
-  const unsigned grid = kv4_grid((long long)a.M * 2 * a.c.H * (a.c.D / Q4_GROUP), num_sms);
-  const bool vec = a.ld % 8 == 0 && a.col[0] % 8 == 0 && a.col[1] % 8 == 0 && ((uintptr_t)a.y & 15u) == 0;
-  if (vec) return launch_pdl(kv_write_q4_kernel<true>, dim3(grid), dim3(KV4_THREADS), 0, s, a);
-  return launch_pdl(kv_write_q4_kernel<false>, dim3(grid), dim3(KV4_THREADS), 0, s, a);
+  const int lanes = kv4_lanes(a.c);
+  const unsigned grid = kv4_grid(a.M, lanes, num_sms);
+  const bool vec = a.ld % 16 == 0 && a.col[0] % 16 == 0 && a.col[1] % 16 == 0 && ((uintptr_t)a.y & 31u) == 0;
+  // (1 / scale stays a normal number in this range)
+  auto pow2 = [](float u) {
+    int e;
+    return std::frexp(u, &e) == 0.5f && e > -100 && e < 100;
+  };
+  const bool exact = !pow2(a.c.unit[0]) || !pow2(a.c.unit[1]);
+  if (vec && !exact) return launch_pdl(kv_write_q4_kernel<true, false>, dim3(grid), dim3(KV4_THREADS), 0, s, a, lanes);
+  if (vec) return launch_pdl(kv_write_q4_kernel<true, true>, dim3(grid), dim3(KV4_THREADS), 0, s, a, lanes);
+  if (!exact) return launch_pdl(kv_write_q4_kernel<false, false>, dim3(grid), dim3(KV4_THREADS), 0, s, a, lanes);
+  return launch_pdl(kv_write_q4_kernel<false, true>, dim3(grid), dim3(KV4_THREADS), 0, s, a, lanes);
 }
 
 cudaError_t launch_kv_read_q4(const Kv4Read &a, int num_sms, cudaStream_t s) {
   if (a.rows <= 0) return cudaSuccess;
-  const unsigned grid = kv4_grid(2ll * a.c.B * a.rows * a.c.H * (a.c.D / Q4_GROUP), num_sms);
-  return launch_pdl(kv_read_q4_kernel, dim3(grid), dim3(KV4_THREADS), 0, s, a);
+  const int lanes = kv4_lanes(a.c);
+  const unsigned grid = kv4_grid((long long)a.c.B * a.rows, lanes, num_sms);
+  if ((((uintptr_t)a.out[0] | (uintptr_t)a.out[1]) & 31u) == 0)
+    return launch_pdl(kv_read_q4_kernel<true>, dim3(grid), dim3(KV4_THREADS), 0, s, a, lanes);
+  return launch_pdl(kv_read_q4_kernel<false>, dim3(grid), dim3(KV4_THREADS), 0, s, a, lanes);
 }
 
 }  // namespace mlora
