@@ -32,15 +32,23 @@ __device__ __forceinline__ int kv4_slot(const Kv4 &c, int b, long long pos) {
   return blk * c.H * c.block_size + (int)(pos - j * c.block_size);
 }
 
-// v / s for the codes.  EXACT: IEEE division.  Otherwise the unit is a power
-// of two, v has 8 significant bits, s 4 and a border between two codes 3, so
-// a quotient that is not on a border is at least 2^-8 of it away: v (1 / s),
-// within 2^-22 of the quotient, rounded to 12 bits falls on the same side, or
+// x / d for a code or a scale, r about 1 / d.  EXACT: IEEE division.  Otherwise
+// the unit is a power of two.  Then x has 8 significant bits, a scale 4 and a
+// border between two codes 3, or 6 unit has 2 and a border between two scales
+// 5: a quotient that is not on a border is at least 2^-8 of it away, so x r,
+// within 2^-21 of the quotient, rounded to 12 bits falls on the same side, or
 // on the border itself.
 template <bool EXACT>
-__device__ __forceinline__ float kv4_ratio(float v, float s, float r) {
-  if (EXACT) return __fdiv_rn(v, s);
-  return __uint_as_float((__float_as_uint(v * r) + 0x800u) & 0xFFFFF000u);
+__device__ __forceinline__ float kv4_ratio(float x, float d, float r) {
+  if (EXACT) return __fdiv_rn(x, d);
+  return __uint_as_float((__float_as_uint(x * r) + 0x800u) & 0xFFFFF000u);
+}
+
+// 1 / d within 2^-22, for d in the range of normal numbers.
+__device__ __forceinline__ float rcp_approx(float d) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
+  return r;
 }
 
 // 32 bytes in one access (32-byte aligned).
@@ -63,23 +71,25 @@ __global__ void __launch_bounds__(KV4_THREADS) kv_write_q4_kernel(const Kv4Write
   grid_dependency_wait();  // y comes from the projection just before
   const int GD = a.c.D / Q4_GROUP, per = a.c.H * GD;
   const int slices = KV4_THREADS / lanes, slice = threadIdx.x / lanes, lane = threadIdx.x - slice * lanes;
-  const int stride = gridDim.x * slices;
-  auto slot_of = [&](int m) {
+  const int stride = gridDim.x * slices, m0 = blockIdx.x * slices + slice;
+  auto slot_of = [&](int k) {  // of the walk's row k
+    const long long m = m0 + (long long)k * stride;
     if (m >= a.M) return -1;
-    const int b = m / a.rows_per_req, t = m - b * a.rows_per_req;
+    const int b = (int)m / a.rows_per_req, t = (int)m - b * a.rows_per_req;
     const int L = __ldg(a.seq_len + b);
     if (L < 0) return -1;  // unused request slot
     const int slot = kv4_slot(a.c, b, (long long)L + a.t0 + t);
-    if (slot < 0 && lane == 0) raise_status(a.c.status, MLORA_DEV_BAD_SLOT);
+    if (slot < 0) raise_status(a.c.status, MLORA_DEV_BAD_SLOT);
     return slot;
   };
-  for (int i = lane; i < 2 * per; i += lanes) {
-    const int kv = i >= per, e = i - (kv ? per : 0), h = e / GD, g = e - h * GD;
-    const float unit = a.c.unit[kv], unit6 = 6.f * unit;
-    const uint16_t *const y = a.y + a.col[kv] + e * Q4_GROUP;
-    uint8_t *const codes = a.c.codes[kv] + (size_t)h * a.c.block_size * (a.c.D / 2) + g * 8;
-    uint8_t *const scales = a.c.scales[kv] + (size_t)h * a.c.block_size * GD + g;
-    int m = blockIdx.x * slices + slice, next = slot_of(m);
+  // (whole warps: the last of them may have lanes without a group)
+  for (int i = lane; (i & ~31) < 2 * per; i += lanes) {
+    const bool mine = i < 2 * per;
+    const int kv = i >= per, e = mine ? i - (kv ? per : 0) : 0, h = e / GD, g = e - h * GD;
+    const float unit = (kv ? a.c.unit[1] : a.c.unit[0]), unit6 = 6.f * unit, inv6 = 1.f / unit6;
+    const uint16_t *const y = a.y + (kv ? a.col[1] : a.col[0]) + e * Q4_GROUP;
+    uint8_t *const codes = (kv ? a.c.codes[1] : a.c.codes[0]) + (size_t)h * a.c.block_size * (a.c.D / 2) + g * 8;
+    uint8_t *const scales = (kv ? a.c.scales[1] : a.c.scales[0]) + (size_t)h * a.c.block_size * GD + g;
     auto fetch = [&](int row, uint32_t (&w)[8]) {
       if (row >= a.M) return;
       const uint16_t *src = y + (size_t)row * a.ld;
@@ -91,22 +101,32 @@ __global__ void __launch_bounds__(KV4_THREADS) kv_write_q4_kernel(const Kv4Write
       }
     };
     uint32_t ahead[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    fetch(m, ahead);
-    for (; m < a.M; m += stride) {
+    fetch(m0, ahead);
+    // The slots of the warp's rows, 32 rows at a time: lane i looks up the i-th.
+    int now = slot_of((int)(threadIdx.x & 31u)), first = 0;
+    auto slot_at = [&](int k) {
+      if (k - first >= 32) {
+        first = k;
+        now = slot_of(k + (int)(threadIdx.x & 31u));
+      }
+      return __shfl_sync(0xffffffffu, now, k - first);
+    };
+    for (int m = m0, k0 = 0; m < a.M; m += stride, ++k0) {
       uint32_t w[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k) w[k] = ahead[k];
       fetch(m + stride, ahead);
-      const int slot = next;
-      next = slot_of(m + stride);
-      if (slot < 0) continue;
+      const int slot = slot_at(k0);
+      if (slot < 0 || !mine) continue;
       // The largest magnitude by its bits: a NaN's lie above every number's, so
       // a NaN anywhere in the group reaches the scale.
       uint32_t mx = 0;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) mx = max(mx, max(w[k] & 0x7FFFu, (w[k] >> 16) & 0x7FFFu));
-      const uint32_t sc = cvt_e4m3(__fdiv_rn(__uint_as_float(mx << 16), unit6));
-      const float s = e4m3_to_float(sc) * unit, r = EXACT ? 0.f : __fdiv_rn(1.f, s);
+      for (int k = 0; k < 8; ++k) mx = __vmaxu2(mx, w[k] & 0x7FFF7FFFu);
+      mx = max(mx & 0xFFFFu, mx >> 16);
+      const uint32_t sc =
+          mx > 0x7F80u ? 0x7Fu : cvt_e4m3(kv4_ratio<EXACT>(__uint_as_float(mx << 16), unit6, inv6));
+      const float s = e4m3_to_float(sc) * unit, r = EXACT ? 0.f : rcp_approx(s);
       uint2 c = make_uint2(0u, 0u);
       if (s != 0.f) {
         float v[8];
@@ -132,65 +152,81 @@ __global__ void __launch_bounds__(KV4_THREADS) kv_read_q4_kernel(const Kv4Read a
   grid_dependency_wait();  // the cache may come from the write just before
   const int GD = a.c.D / Q4_GROUP, per = a.c.H * GD, M = a.c.B * a.rows;
   const int slices = KV4_THREADS / lanes, slice = threadIdx.x / lanes, lane = threadIdx.x - slice * lanes;
-  const long long stride = (long long)gridDim.x * slices;
-  auto slot_of = [&](long long m) {
+  const int stride = gridDim.x * slices, m0 = blockIdx.x * slices + slice;
+  auto slot_of = [&](int k) {  // of the walk's row k
+    const long long m = m0 + (long long)k * stride;
     if (m >= M) return -1;
     const int b = (int)m / a.rows, t = (int)m - b * a.rows;
     const int L = __ldg(a.start + b);
     const long long pos = (long long)L + t;
     if (L < 0 || pos >= __ldg(a.end + b)) return -1;
     const int slot = kv4_slot(a.c, b, pos);
-    if (slot < 0 && lane == 0) raise_status(a.c.status, MLORA_DEV_BAD_SLOT);
+    if (slot < 0) raise_status(a.c.status, MLORA_DEV_BAD_SLOT);
     return slot;
   };
-  for (int i = lane; i < 2 * per; i += lanes) {
-    const int kv = i >= per, e = i - (kv ? per : 0), h = e / GD, g = e - h * GD;
-    const float unit = a.c.unit[kv];
-    const uint8_t *const codes = a.c.codes[kv] + (size_t)h * a.c.block_size * (a.c.D / 2) + g * 8;
-    const uint8_t *const scales = a.c.scales[kv] + (size_t)h * a.c.block_size * GD + g;
-    // Two rows ahead: a row's codes are asked for while the row before is written.
-    long long m = (long long)blockIdx.x * slices + slice;
-    int next = slot_of(m), after = slot_of(m + stride);
-    uint2 c1 = make_uint2(0, 0);
-    uint32_t s1 = 0;
-    auto ask = [&](int slot) {
-      c1 = make_uint2(0, 0);
-      s1 = 0;
-      if (slot >= 0) {
-        c1 = __ldg(reinterpret_cast<const uint2 *>(codes + (size_t)slot * (a.c.D / 2)));
-        s1 = __ldg(scales + (size_t)slot * GD);
+  // (whole warps: the last of them may have lanes without a group)
+  for (int i = lane; (i & ~31) < 2 * per; i += lanes) {
+    const bool mine = i < 2 * per;
+    const int kv = i >= per, e = mine ? i - (kv ? per : 0) : 0, h = e / GD, g = e - h * GD;
+    const float unit = (kv ? a.c.unit[1] : a.c.unit[0]);
+    const uint8_t *const codes = (kv ? a.c.codes[1] : a.c.codes[0]) + (size_t)h * a.c.block_size * (a.c.D / 2) + g * 8;
+    const uint8_t *const scales = (kv ? a.c.scales[1] : a.c.scales[0]) + (size_t)h * a.c.block_size * GD + g;
+    // The slots of the warp's rows, 32 rows at a time: lane i looks up the i-th.
+    int now = slot_of((int)(threadIdx.x & 31u)), first = 0;
+    auto slot_at = [&](int k) {
+      if (k - first >= 32) {
+        first = k;
+        now = slot_of(k + (int)(threadIdx.x & 31u));
+      }
+      return __shfl_sync(0xffffffffu, now, k - first);
+    };
+    // A row's codes are asked for while the two before it are written.
+    int slot[2];
+    uint2 c[2];
+    uint32_t sc[2];
+    auto ask = [&](int k, int n) {
+      slot[n] = slot_at(k);
+      c[n] = make_uint2(0, 0);
+      sc[n] = 0;
+      if (slot[n] >= 0) {
+        c[n] = __ldg(reinterpret_cast<const uint2 *>(codes + (size_t)slot[n] * (a.c.D / 2)));
+        sc[n] = __ldg(scales + (size_t)slot[n] * GD);
       }
     };
-    ask(next);
-    for (; m < M; m += stride) {
-      const int slot = next;
-      const uint2 c = c1;
-      const uint32_t sc = s1;
-      next = after;
-      ask(next);
-      after = slot_of(m + 2 * stride);
+    auto put = [&](long long m, int n) {
+      if (m >= M || !mine) return;
       uint32_t w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-      if (slot >= 0) {
-        const float s = e4m3_to_float(sc);
+      if (slot[n] >= 0) {
+        const float s = e4m3_to_float(sc[n]);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           uint32_t f[4];
-          e2m1x8_to_f16(half ? c.y : c.x, f);
+          e2m1x8_to_f16(half ? c[n].y : c[n].x, f);
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             // code * scale is exact; the product with unit is rounded to fp32
             // (exact for a power of two), then once to bf16.
-            w[4 * half + k] = (uint32_t)float_to_bf16_bits(f16_lo(f[k]) * s * unit) |
-                              ((uint32_t)float_to_bf16_bits(f16_hi(f[k]) * s * unit) << 16);
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;"
+                : "=r"(w[4 * half + k])
+                : "f"(f16_hi(f[k]) * s * unit), "f"(f16_lo(f[k]) * s * unit));
         }
       }
-      uint4 *dst = reinterpret_cast<uint4 *>(a.out[kv] + ((size_t)m * per + e) * Q4_GROUP);
+      uint4 *dst = reinterpret_cast<uint4 *>((kv ? a.out[1] : a.out[0]) + ((size_t)m * per + e) * Q4_GROUP);
       if (VEC) {
         stg_32(dst, w);
       } else {
         dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
         dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
       }
+    };
+    ask(0, 0);
+    ask(1, 1);
+    long long m = m0;
+    for (int k = 0; m < M; k += 2, m += 2ll * stride) {
+      put(m, 0);
+      ask(k + 2, 0);
+      put(m + stride, 1);
+      ask(k + 3, 1);
     }
   }
 }
