@@ -1,0 +1,240 @@
+// What the attention kernels on tcgen05 share: the operands' layout in shared
+// memory, their descriptors, tensor memory in and out, and the boxes by which
+// TMA reads the cache.
+#pragma once
+
+#include "attn_common.cuh"
+#include "e2m1.cuh"
+
+namespace mlora {
+
+constexpr int AP_TILE = 128;
+constexpr int AP_GROUPS = 4;   // of 32 positions in a tile
+constexpr float AP_SLACK = 8.f;
+constexpr float AP_NONE = -__builtin_huge_valf();
+
+// How a tile's K and V come: by TMA boxes of a page's positions, by a gather of
+// 16-byte pieces, or as codes of the 4-bit cache.
+enum { AP_BOXES = 0, AP_PIECES = 1, AP_CODES = 2 };
+
+// An operand's 128 rows of D elements: groups of 8 rows, in each the row's
+// 64-element blocks side by side as 1024-byte swizzle patterns, so that any
+// multiple of 8 positions with all their elements is one run of memory and
+// one TMA box.
+template <int D>
+struct ApOperand {
+  static constexpr int GROUP = 1024 * (D / 64);
+  static constexpr int BYTES = AP_TILE / 8 * GROUP;
+};
+
+// Byte offset of a row's 16-byte piece in an operand.
+template <int D>
+__device__ __forceinline__ int ap_at(int row, int piece) {
+  return (row >> 3) * ApOperand<D>::GROUP + (piece >> 3) * 1024 + (row & 7) * 128 + ((piece ^ row) & 7) * 16;
+}
+
+__device__ __forceinline__ void ap_cp_async_16(uint32_t dst, const void *src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void ap_cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Tensor memory to registers, load and wait in one statement: between the two
+// the registers are not yet what the compiler takes them for (it may move or
+// spill them).
+__device__ __forceinline__ void tmem_get(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "{\n\ttcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15},"
+      " [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;\n\t}"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_get(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "{\n\ttcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,"
+      "%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
+      "tcgen05.wait::ld.sync.aligned;\n\t}"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_get(uint32_t taddr, uint32_t (&r)[64]) {
+  asm volatile(
+      "{\n\ttcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,"
+      "%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,"
+      "%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];\n\t"
+      "tcgen05.wait::ld.sync.aligned;\n\t}"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]),
+        "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]),
+        "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]),
+        "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]),
+        "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+      : "r"(taddr)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+          taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_x32(uint32_t taddr, const uint32_t *r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// D[tmem] (+)= A[tmem] * B[smem], 16-bit inputs, fp32 accumulator, one CTA.
+__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                           uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// v = x * mul + add, two at a time.
+__device__ __forceinline__ void fma_x32(float (&v)[32], const uint32_t *x, float mul, float add) {
+  uint64_t m2, a2;
+  asm("mov.b64 %0, {%1, %1};" : "=l"(m2) : "f"(mul));
+  asm("mov.b64 %0, {%1, %1};" : "=l"(a2) : "f"(add));
+#pragma unroll
+  for (int i = 0; i < 32; i += 2) {
+    uint64_t y;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "r"(x[i]), "r"(x[i + 1]));
+    asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(y) : "l"(m2), "l"(a2));
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(v[i]), "=f"(v[i + 1]) : "l"(y));
+  }
+}
+// The largest of 64 values (NaN left out).
+__device__ __forceinline__ float max_x64(const uint32_t (&x)[64]) {
+  float m[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    m[k] = __uint_as_float(x[8 * k + 7]);
+#pragma unroll
+    for (int i = 0; i < 6; i += 2)
+      asm("max.f32 %0, %0, %1, %2;"
+          : "+f"(m[k])
+          : "f"(__uint_as_float(x[8 * k + i])), "f"(__uint_as_float(x[8 * k + i + 1])));
+    m[k] = fmaxf(m[k], __uint_as_float(x[8 * k + 6]));
+  }
+#pragma unroll
+  for (int n = 4; n > 0; n >>= 1)
+#pragma unroll
+    for (int k = 0; k < n; ++k) m[k] = fmaxf(m[k], m[k + n]);
+  return m[0];
+}
+__device__ __forceinline__ float sum_x32(const float (&v)[32]) {
+  uint64_t y[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) asm("mov.b64 %0, {%1, %2};" : "=l"(y[i]) : "f"(v[2 * i]), "f"(v[2 * i + 1]));
+#pragma unroll
+  for (int n = 8; n > 0; n >>= 1)
+#pragma unroll
+    for (int i = 0; i < n; ++i) asm("add.rn.f32x2 %0, %0, %1;" : "+l"(y[i]) : "l"(y[i + n]));
+  float a, b;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(y[0]));
+  return a + b;
+}
+
+// Q's and K's operands, K-major: the groups of 8 rows are the stride offset
+// apart, the blocks are stepped over by address.
+template <int D>
+__device__ __forceinline__ uint64_t ap_desc_k_major(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)1 << 16;                              // leading byte offset (unused)
+  d |= (uint64_t)(ApOperand<D>::GROUP >> 4) << 32;         // stride byte offset
+  d |= (uint64_t)1 << 46;                              // descriptor version
+  d |= (uint64_t)2 << 61;                              // 128-byte swizzle
+  return d;
+}
+
+// V's tile as the second product's B operand: 16 positions (K) by D elements
+// (N), N contiguous: 8 positions are the stride offset apart, the next 64
+// elements the leading offset.
+template <int D>
+__device__ __forceinline__ uint64_t ap_desc_n_major(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)(1024 >> 4) << 16;                    // leading byte offset
+  d |= (uint64_t)(ApOperand<D>::GROUP >> 4) << 32;         // stride byte offset
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+
+template <bool F16>
+__host__ __device__ constexpr uint32_t ap_idesc(int N, bool b_n_major) {
+  return (1u << 4) | ((F16 ? 0u : 1u) << 7) | ((F16 ? 0u : 1u) << 10) | ((b_n_major ? 1u : 0u) << 16) |
+         ((uint32_t)(N >> 3) << 17) | ((128u >> 4) << 24);
+}
+
+template <bool F16>
+__device__ __forceinline__ uint32_t ap_pack2(float lo, float hi) {
+  uint32_t r;
+  if (F16)
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t ap_hmul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+typedef CUresult (*ApEncodeFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                               const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                               CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// A cache as (64 elements, 8 slots, D / 64 blocks, slots / 8, H): a box is one
+// head's elements of 8 n slots, in the order of an operand's groups.
+inline bool ap_map(CUtensorMap *map, const void *base, const AttnArgs &a, int box) {
+  static ApEncodeFn fn = nullptr;
+  if (!fn) {
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<ApEncodeFn>(p);
+    if (!fn) return false;
+  }
+  const cuuint64_t row = (cuuint64_t)a.H * a.D * 2;
+  cuuint64_t dims[5] = {64, 8, (cuuint64_t)a.D / 64, (cuuint64_t)a.num_blocks * a.block_size / 8, (cuuint64_t)a.H};
+  cuuint64_t strides[4] = {row, 128, 8 * row, (cuuint64_t)a.D * 2};
+  cuuint32_t boxes[5] = {64, 8, (cuuint32_t)a.D / 64, (cuuint32_t)box / 8, 1};
+  cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void *>(base), dims, strides, boxes, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace mlora
