@@ -682,7 +682,7 @@ size_t mlora_attention_workspace_bytes(int M, int rows_per_req, int Hq, int H, i
   if (!attn_heads_ok(M, rows_per_req, Hq, H, D)) return 0;
   int sms = device_sms();
   if (sms <= 0) sms = 160;
-  return align_up(WS_SCRATCH_OFF + (attn_head_fast(D) ? attn_rows_scratch_bytes(D, sms) : 0), 256);
+  return align_up(WS_SCRATCH_OFF + (attn_head_fast(D) ? std::max(attn_rows_scratch_bytes(D, sms), attn_wide_scratch_bytes(D, sms)) : 0), 256);
 }
 
 static mlora_status attention_impl(const void *y, int M, int ld, int q_col, int Hq, int H, int D, const void *k,
@@ -733,6 +733,9 @@ static mlora_status attention_impl(const void *y, int M, int ld, int q_col, int 
   uint8_t *ws = (uint8_t *)workspace;
   const bool fast = attn_head_fast(D) && ld % 8 == 0 && q_col % 8 == 0 && aligned(y, 16) && aligned(k, 16) && aligned(v, 16);
   if (fast && (long long)rows_per_req * (Hq / H) >= 64) return cuda_status(launch_attn_prompt(a, q4, (cudaStream_t)stream));
+  if (fast && (long long)rows_per_req * (Hq / H) > 16 && attn_wide_takes(a, q4))
+    return cuda_status(launch_attn_wide(a, q4, reinterpret_cast<float *>(ws + WS_SCRATCH_OFF),
+                                        reinterpret_cast<uint32_t *>(ws + WS_COUNTERS_OFF), sms, (cudaStream_t)stream));
   if (fast)
     return cuda_status(launch_attn_rows(a, q4, reinterpret_cast<float *>(ws + WS_SCRATCH_OFF),
                                         reinterpret_cast<uint32_t *>(ws + WS_COUNTERS_OFF), sms, (cudaStream_t)stream));

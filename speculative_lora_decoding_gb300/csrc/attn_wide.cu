@@ -1,0 +1,983 @@
+// Attention for some tens of rows per (request, cache head) (verify passes with
+// grouped heads): heads of 64 and 128 on tcgen05, over the bf16 or the 4-bit
+// paged cache.
+//
+// 25 query rows against a cache head are too many for the register MMAs of
+// attn_rows.cu (over the 4-bit cache those bound a pass at 3/4 of HBM before
+// anything else is counted) and too few for rows on the M side of a tcgen05
+// MMA.  Here the cache is the M side and the rows the N side:
+//   S^T[128 positions, rows] = K Q^T,   O^T[D, rows] += V^T P^T,
+// all operands in shared memory, S^T and O^T in tensor memory, so the threads
+// do one score per (position, row) and nothing else: with positions in lanes
+// every lane has work whatever the number of rows.
+//
+// A CTA (one per SM) has a contiguous share of all (request, head, tile)
+// triples, found on the device as in attn_rows.cu; units that cuts go through
+// are joined by the last CTA to arrive.  Warps 0-3 take the exponentials (a
+// position each), warp 4 issues the MMAs, the others bring tiles: TMA boxes, or
+// codes expanded to fp16.  The running maxima move, by whole numbers, when a
+// score exceeds its row's by 8.
+#include "attn_tc.cuh"
+
+namespace mlora {
+
+constexpr int AW_MMA_WARP = 8, AW_Q_WARP = 9, AW_AHEAD = 3;
+__host__ __device__ constexpr int aw_loaders(int mode) { return mode == AP_BOXES ? 1 : 8; }
+__host__ __device__ constexpr int aw_threads(int mode) { return 32 * (AW_Q_WARP + 1 + aw_loaders(mode)); }
+
+template <int D, int NC>
+struct AwCfg {
+  static constexpr int GROUP = ApOperand<D>::GROUP, OPERAND = ApOperand<D>::BYTES;
+  static constexpr int Q_BYTES = NC / 8 * GROUP;        // NC rows of D elements
+  static constexpr int P_BYTES = NC / 8 * ApOperand<128>::GROUP;  // NC rows of 128 positions
+  static constexpr int K_OFF = 0;                       // two stages
+  static constexpr int V_OFF = 2 * OPERAND;             // two stages
+  static constexpr int Q_OFF = 4 * OPERAND;             // of this segment and the next
+  static constexpr int P_OFF = Q_OFF + 2 * Q_BYTES;     // of this tile and the next
+  static constexpr int SH_OFF = P_OFF + 2 * P_BYTES;
+  static constexpr int RAW_OFF = SH_OFF + 8192;         // codes on their way, a place per warp and tile
+  static constexpr int RAW_BYTES = 32 * (D / 2 + D / 16);
+  static constexpr int smem(bool q4) { return RAW_OFF + (q4 ? 8 * AW_AHEAD * RAW_BYTES : 0) + 1024; }  // (and the alignment)
+  // A part of a unit: NC (maximum, sum) pairs, then NC x D.
+  static constexpr int SLOT = 2 * NC + NC * D;
+};
+
+template <int NC>
+struct __align__(16) AwShared {
+  uint64_t q_full[2], q_empty[2], k_full[2], k_empty[2], v_full[2], s_full[2], p_full[2], pv_done[2], fin;
+  uint32_t tmem;
+  int abort, last[2], joins;
+  long long bound[2], at_unit[2], sums[20];
+  int at_b[2], at_u[2], at_tile[2];
+  alignas(16) uint32_t there[4][AP_GROUPS];
+  alignas(16) int scales[2][AP_GROUPS];  // whether some scale of V is not finite
+  int odd[2];
+  // per row (column of S^T): what the scores are multiplied by, the first and
+  // last positions it sees, per segment parity; the running maximum's negative
+  // and whether it is there; what moves it; partial sums of a warp
+  alignas(16) float mul[2][NC];
+  alignas(16) int hi[2][NC], lo[2][NC];
+  alignas(16) float2 coef[NC];
+  int set[NC];
+  alignas(16) float2 move[NC];
+  float part[4][NC];
+  // at a unit's end: what a row's sums are multiplied by (-1: no weights), and
+  // its place in `out`
+  alignas(16) float inv[NC];
+  int row[NC];
+};
+
+struct AwArgs {
+  AttnArgs a;
+  int G, n_rt, RT;
+  uint32_t G_magic;
+  int extent, bs_shift, box_log2;
+  float *part;  // two slots per CTA
+  uint32_t *counters;
+};
+
+template <int BYTES>
+__device__ __forceinline__ void aw_cp_async_small(uint32_t dst, const void *src, bool there) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES), "r"(there ? BYTES : 0)
+               : "memory");
+}
+
+template <int MODE, int D, int NC>
+__global__ void __launch_bounds__(aw_threads(MODE), 1)
+    attn_wide_kernel(const AwArgs p, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
+  using C = AwCfg<D, NC>;
+  constexpr bool Q4 = MODE == AP_CODES;
+  constexpr int LOADERS = aw_loaders(MODE), THREADS = aw_threads(MODE), WARPS = THREADS / 32;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = align_smem_1024(smem_raw);
+  static_assert(sizeof(AwShared<NC>) <= 8192, "AwShared");
+  AwShared<NC> &sh = *reinterpret_cast<AwShared<NC> *>(smem + C::SH_OFF);
+  const AttnArgs &a = p.a;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int cta = blockIdx.x, T = a.rows_per_req, U = a.H * p.n_rt;
+
+  grid_dependency_wait();  // y, the cache and the lengths come from the kernels just before
+
+  auto per_head = [&](int r) { return div_heads(r, p.G, p.G_magic); };
+  auto rows_of = [&](int b) { return min(T, a.M - b * T); };
+  auto range_of = [&](int b) {
+    const int tb = rows_of(b);
+    const int L = b < a.B && tb > 0 ? __ldg(a.seq_len + b) : -1;
+    if (L < 0) return AttnRange{0, 0, 0, 0, 0};
+    const long long p0 = (long long)L + a.t0;
+    return attn_range<AP_TILE>(p0, p0 + tb - 1, a.window, a.sinks, p.extent);
+  };
+  // Requests that see nothing: zeros.  Rows past the table's reach: status.
+  for (int b = cta; b < a.B; b += gridDim.x) {
+    const int tb = rows_of(b);
+    if (tb <= 0) break;
+    if (range_of(b).nt == 0) {
+      uint4 *dst = reinterpret_cast<uint4 *>(a.out + (size_t)b * T * a.Hq * D);
+      const size_t n = (size_t)tb * a.Hq * D / 8;
+      for (size_t i = tid; i < n; i += THREADS) dst[i] = make_uint4(0, 0, 0, 0);
+    }
+    if (tid == 0) {
+      const int L = __ldg(a.seq_len + b);
+      if (L >= 0 && (long long)L + a.t0 + tb > p.extent) raise_status(a.status, MLORA_DEV_BAD_SLOT);
+    }
+  }
+
+  // --- the share ---------------------------------------------------------------
+  // Units are cut up by time: a unit's start counts as START tiles.  A request's
+  // tiles (of one unit) and whether it has any, in one number.
+  constexpr int START = 2, BITS = 20;
+  auto counted = [&](int b) {
+    const int nt = b < a.B ? range_of(b).nt : 0;
+    return nt ? ((long long)(nt + START) << BITS) + 1 : 0ll;
+  };
+  long long total = 0;
+  const long long mine = counted(tid);
+  for (int base = 0; base < a.B; base += THREADS) {
+    long long v = base == 0 ? mine : counted(base + tid);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    total += v;
+  }
+  if (lane == 0) sh.sums[warp] = total;
+  __syncthreads();
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) total += sh.sums[w];
+  const int used = (int)(total & ((1 << BITS) - 1));
+  total = (total >> BITS) * U;
+  // A CTA per unit while they are few and short (4 tiles).
+  const int P = (int)min((long long)gridDim.x, max(total / 4, (long long)used * U));
+  if (cta >= P) return;
+  const long long quot = total < (1ll << 31) ? (long long)((uint32_t)total / (uint32_t)P) : total / P;
+  const int rest = (int)(total - quot * P);
+  auto raw_cut = [&](int x) { return quot * x + (uint32_t)(rest * x) / (uint32_t)P; };
+  const int near = (int)min(quot / 16, 1ll << 20) + 1;
+  // The tile of a unit that starts at `unit` and has nt tiles where CTA x's share
+  // begins: 0 if before it, nt if after it; cuts near an end of the unit go there.
+  auto cut_in = [&](long long raw, long long unit, int nt) {
+    const long long in = raw - unit - START;
+    if (in <= 0) return 0;
+    if (in >= nt) return nt;
+    const int o = (int)in;
+    if (o < near || nt - o < near) return 2 * o < nt ? 0 : nt;
+    return o;
+  };
+  long long *ends = reinterpret_cast<long long *>(smem);  // the sums of `counted` up to a request
+  {
+    long long before = 0;
+    for (int base = 0; base < a.B; base += THREADS) {
+      __syncthreads();
+      long long v = base == 0 ? mine : counted(base + tid);
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long u = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += u;
+      }
+      if (lane == 31) sh.sums[warp] = v;
+      __syncthreads();
+      long long off = before, all = before;
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) {
+        if (w < warp) off += sh.sums[w];
+        all += sh.sums[w];
+      }
+      ends[tid] = off + v;
+      __syncthreads();
+      if (tid < 2) {
+        const long long raw = raw_cut(cta + tid);
+        if (raw == total) {
+          sh.bound[tid] = total - (long long)used * U * START;
+        } else if ((before >> BITS) * U <= raw && raw < (all >> BITS) * U) {
+          int x = 0;  // the first request that ends past the cut
+#pragma unroll
+          for (int step = 512; step > 0; step >>= 1)
+            if (x + step <= THREADS && (ends[x + step - 1] >> BITS) * U <= raw) x += step;
+          const long long start = x > 0 ? ends[x - 1] : before;
+          const int n = (int)((ends[x] >> BITS) - (start >> BITS)), nt = n - START;
+          const long long unit0 = (start >> BITS) * U, in = raw - unit0;
+          const int u = in < (1ll << 31) ? (int)((uint32_t)in / (uint32_t)n) : (int)(in / n);
+          const long long unit = unit0 + (long long)u * n;
+          const int o = cut_in(raw, unit, nt);
+          sh.at_b[tid] = base + x;
+          sh.at_u[tid] = u;
+          sh.at_tile[tid] = o;
+          sh.at_unit[tid] = unit;
+          // (in tiles: less what the units up to this one count more)
+          sh.bound[tid] = unit - START * ((start & ((1 << BITS) - 1)) * U + u) + o;
+        }
+      }
+      before = all;
+    }
+    __syncthreads();
+  }
+  const int count = (int)(sh.bound[1] - sh.bound[0]);
+  if (count == 0) return;
+
+  struct Segment {
+    int i;           // tiles of the CTA's share before it
+    long long unit;  // where its unit starts
+    int b, h, rt, tile, end, nt;
+    AttnRange r;
+  };
+  auto close = [&](Segment &s) { s.end = min(s.nt, s.tile + count - s.i); };
+  auto to_next_unit = [&](Segment &s) {
+    s.tile = 0;
+    s.unit += s.nt + START;
+    if (++s.rt < p.n_rt) return;
+    s.rt = 0;
+    if (++s.h < a.H) return;
+    s.h = 0;
+    do {
+      ++s.b;
+      s.r = range_of(s.b);
+    } while (s.r.nt == 0 && s.b < a.B);
+    s.nt = s.r.nt;
+  };
+  auto begin = [&]() {
+    Segment s;
+    s.i = 0;
+    s.unit = sh.at_unit[0];
+    s.b = sh.at_b[0];
+    s.r = range_of(s.b);
+    s.nt = s.r.nt;
+    s.h = sh.at_u[0] / p.n_rt;
+    s.rt = sh.at_u[0] - s.h * p.n_rt;
+    s.tile = sh.at_tile[0];
+    if (s.tile == s.nt) to_next_unit(s);  // a cut that moved to a unit's end
+    close(s);
+    return s;
+  };
+  auto next_segment = [&](Segment &s) {  // false: that was the last
+    s.i += s.end - s.tile;
+    if (s.i >= count) return false;
+    to_next_unit(s);
+    close(s);
+    return true;
+  };
+  auto rows_in = [&](const Segment &s) { return max(0, min(p.RT, rows_of(s.b) * p.G - s.rt * p.RT)); };
+  // Whether some row of the segment's unit does not see all of tile j: the
+  // positions that all rows see, but for the sinks, are those in (above, below].
+  struct Seen {
+    int below, above;
+  };
+  auto seen_of = [&](const Segment &s) {
+    const long long p0 = (long long)__ldg(a.seq_len + s.b) + a.t0;
+    const int r0 = s.rt * p.RT, n = rows_in(s);
+    const long long p_lo = p0 + per_head(r0), p_hi = p0 + per_head(r0 + max(n, 1) - 1);
+    Seen x;
+    x.below = (int)min(p_lo, 0x7ffffff0ll);
+    x.above = a.window ? (int)min(max(p_hi - a.window, -1ll), 0x7ffffff0ll) : -1;
+    return x;
+  };
+  auto partial = [&](const Seen &x, int j0) { return j0 + AP_TILE - 1 > x.below || (j0 <= x.above && j0 + AP_TILE - 1 >= a.sinks); };
+
+  if (tid == 0) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.q_full[i], 1);
+      mbar_init(&sh.q_empty[i], 8);
+      mbar_init(&sh.k_full[i], MODE == AP_BOXES ? 1 : AP_GROUPS);
+      mbar_init(&sh.v_full[i], MODE == AP_BOXES ? 1 : AP_GROUPS);
+      mbar_init(&sh.k_empty[i], 1);
+      mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.p_full[i], 8);
+      mbar_init(&sh.pv_done[i], 1);
+    }
+    mbar_init(&sh.fin, 1);
+    sh.abort = 0;
+#pragma unroll
+    for (int i = 0; i < 2 * AP_GROUPS; ++i) (&sh.scales[0][0])[i] = 0;
+    fence_mbar_init();
+  }
+  if (warp == AW_MMA_WARP) {
+    tmem_alloc(&sh.tmem, 256);
+    tmem_relinquish();
+  }
+  fence_proxy_async_smem();  // `ends`, before the copies there
+  tc_fence_before_sync();
+  block_sync();
+  tc_fence_after_sync();
+  // Kernels that follow may take tensor memory only when this CTA has its own.
+  grid_launch_dependents();
+  const uint32_t tmem = sh.tmem;
+  volatile int *abort = &sh.abort;
+  auto wait = [&](uint64_t *bar, uint32_t parity) {
+    if (mbar_try_wait(bar, parity & 1u)) return true;
+    if (*abort) return false;
+    if (mbar_wait_bounded(bar, parity & 1u, abort)) return true;
+    *abort = 1;
+    return false;
+  };
+  // S^T of tile i at column 64 (i & 1), O^T at column 128.
+  constexpr uint32_t O_COL = 128;
+
+  if (warp < AW_MMA_WARP) {
+    // --- scores and weights -------------------------------
+    // (A wait that gives up leaves the results wrong, not the warps' steps: they
+    // meet at barriers.)
+    // Four warps have the first half of the rows, four the second: each thread a
+    // position's HC scores.
+    constexpr int HC = NC / 2;
+    const int half = warp >> 2, quarter = warp & 3, ht = tid & 127, cb = half * HC;
+    const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+    auto half_sync = [&]() { named_bar_sync(1 + half, 128); };
+    Segment seg = begin();
+    int it = 0;
+    for (int n = 0;; ++n) {
+      const int par = n & 1;
+      const Seen sn = seen_of(seg);
+      const int n_rows = rows_in(seg);
+      if (ht < HC) sh.set[cb + ht] = 0;
+      wait(&sh.q_full[par], n >> 1);
+      half_sync();
+      float l[HC];
+#pragma unroll
+      for (int c = 0; c < HC; ++c) l[c] = 0.f;
+
+      for (int j = seg.tile; j < seg.end; ++j, ++it) {
+        wait(&sh.s_full[it & 1], it >> 1);
+        tc_fence_after_sync();
+        const int j0 = attn_tile_start<AP_TILE>(seg.r, j), pos = j0 + ht;
+        const bool part = partial(sn, j0);
+        const uint32_t *there = sh.there[it & 3];
+        const bool all = (there[0] & there[1] & there[2] & there[3]) == 0xffffffffu;
+        const bool here = (there[quarter] >> lane) & 1u;
+        uint32_t x[HC];
+        tmem_get(tmem + lanes + 64 * (it & 1) + cb, x);
+        float d[HC];
+        bool far = j == seg.tile;
+        if (far) {
+#pragma unroll
+          for (int c = 0; c < HC; ++c) d[c] = __uint_as_float(x[c]) * sh.mul[par][cb + c];
+        } else {
+#pragma unroll
+          for (int c = 0; c < HC; c += 2) {
+            const float4 k = *reinterpret_cast<const float4 *>(&sh.coef[cb + c]);
+            d[c] = fmaf(__uint_as_float(x[c]), k.x, k.y);
+            d[c + 1] = fmaf(__uint_as_float(x[c + 1]), k.z, k.w);
+          }
+        }
+        if (part || !all) {
+          const bool sink = pos < a.sinks;
+#pragma unroll
+          for (int c = 0; c < HC; c += 4) {
+            const int4 hi = *reinterpret_cast<const int4 *>(&sh.hi[par][cb + c]), lo = *reinterpret_cast<const int4 *>(&sh.lo[par][cb + c]);
+            const int his[4] = {hi.x, hi.y, hi.z, hi.w}, los[4] = {lo.x, lo.y, lo.z, lo.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const bool vis = here & (pos <= his[k]) & ((pos > los[k]) | sink);
+              d[c + k] = vis ? d[c + k] : AP_NONE;
+            }
+          }
+        }
+        float mx[4] = {AP_NONE, AP_NONE, AP_NONE, AP_NONE};
+#pragma unroll
+        for (int c = 0; c < HC; ++c) mx[c & 3] = fmaxf(mx[c & 3], d[c]);
+        far |= fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) > AP_SLACK;
+        // (rows without a maximum have coefficients for a maximum of 0; whatever
+        // they see for the first time moves it)
+        if (!far && sh.last[half]) {
+#pragma unroll
+          for (int c = 0; c < HC; ++c) far |= !sh.set[cb + c] && d[c] > AP_NONE;
+        }
+        if (!named_bar_and(3 + half, 128, !far)) {
+#pragma unroll
+          for (int c = 0; c < HC; ++c) {
+            float v;
+            asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(v) : "f"(d[c]));
+            if (lane == 0) sh.part[quarter][cb + c] = v;
+          }
+          half_sync();
+          if (ht < HC) {
+            const int c = cb + ht;
+            const float v = fmaxf(fmaxf(sh.part[0][c], sh.part[1][c]), fmaxf(sh.part[2][c], sh.part[3][c]));
+            const bool set = sh.set[c] != 0, go = v > AP_NONE && (!set || v > AP_SLACK);
+            const float by = go ? floorf(v) : 0.f;
+            sh.move[c] = make_float2(by, set && go ? exp2_weight(-by) : 1.f);
+            const float old = j == seg.tile ? 0.f : sh.coef[c].y;
+            sh.coef[c] = make_float2(sh.mul[par][c], old - by);
+            if (go) sh.set[c] = 1;
+          }
+          half_sync();
+          if (quarter == 0) {  // whether some row still has no maximum
+            int unset = 0;
+            if (lane < HC && cb + lane < n_rows) unset = !sh.set[cb + lane];
+            unset = __any_sync(0xffffffffu, unset);
+            if (lane == 0) sh.last[half] = unset;
+          }
+#pragma unroll
+          for (int c = 0; c < HC; ++c) {
+            const float2 k = sh.move[cb + c];
+            d[c] -= k.x;
+            l[c] *= k.y;
+          }
+          if (j > seg.tile) {
+            wait(&sh.pv_done[(it - 1) & 1], (it - 1) >> 1);
+            tc_fence_after_sync();
+#pragma unroll
+            for (int c = 0; c < HC; c += 16) {
+              uint32_t o[16];
+              tmem_get(tmem + lanes + O_COL + cb + c, o);
+#pragma unroll
+              for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * sh.move[cb + c + k].y);
+              tmem_st_x16(tmem + lanes + O_COL + cb + c, o);
+            }
+            tmem_st_wait();
+          }
+          half_sync();  // what moved is written again later
+        }
+        if (it >= 2) wait(&sh.pv_done[it & 1], (it - 2) >> 1);  // P's place is free
+        uint8_t *P = smem + C::P_OFF + (it & 1) * C::P_BYTES + (cb >> 3) * 2048 + (ht >> 6) * 1024 + (ht & 7) * 2;
+        const uint32_t swz = (uint32_t)(ht >> 3) & 7u;
+#pragma unroll
+        for (int c = 0; c < HC; c += 2) {
+          const float w0 = exp2_weight(d[c]), w1 = exp2_weight(d[c + 1]);
+          l[c] += w0;
+          l[c + 1] += w1;
+          const uint32_t two = ap_pack2<Q4>(w0, w1);
+          *reinterpret_cast<uint16_t *>(P + (c >> 3) * 2048 + (c & 7) * 128 + ((swz ^ (c & 7)) * 16)) = (uint16_t)two;
+          *reinterpret_cast<uint16_t *>(P + (c >> 3) * 2048 + ((c + 1) & 7) * 128 + ((swz ^ ((c + 1) & 7)) * 16)) =
+              (uint16_t)(two >> 16);
+        }
+        bool odd = false;
+        if (part) {
+          wait(&sh.v_full[it & 1], it >> 1);
+          if (Q4) {
+            const int4 f = *reinterpret_cast<const int4 *>(sh.scales[it & 1]);
+            odd = (f.x | f.y | f.z | f.w) != 0;
+          } else {
+            const uint4 *v = reinterpret_cast<const uint4 *>(smem + C::V_OFF + (it & 1) * C::OPERAND);
+#pragma unroll
+            for (int k = 0; k < C::OPERAND / 16; k += 256) {
+              const uint4 q = v[k + tid];
+              const uint32_t e[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+              for (int n = 0; n < 4; ++n) odd |= ((e[n] & 0x7F80u) == 0x7F80u) | ((e[n] & 0x7F800000u) == 0x7F800000u);
+            }
+          }
+          odd = !named_bar_and(5, 256, !odd);
+        }
+        if (tid == 0) sh.odd[it & 1] = odd;
+        if (odd) {
+          // Values that are not finite and that some rows do not see: the
+          // product would bring 0 times them to those rows.  The tile is added
+          // up here (the MMA warp leaves it out), a thread per element of D.
+          half_sync();  // P is whole
+          if (j > seg.tile) {
+            wait(&sh.pv_done[(it - 1) & 1], (it - 1) >> 1);
+            tc_fence_after_sync();
+          }
+          const uint8_t *Pt = smem + C::P_OFF + (it & 1) * C::P_BYTES, *V = smem + C::V_OFF + (it & 1) * C::OPERAND;
+          const int e = ht & (D - 1);
+          for (int c0 = cb; c0 < cb + HC; c0 += 16) {
+            uint32_t o[16];
+            if (j > seg.tile) {
+              tmem_get(tmem + lanes + O_COL + c0, o);
+            } else {
+#pragma unroll
+              for (int k = 0; k < 16; ++k) o[k] = 0;
+            }
+            for (int jj = 0; jj < AP_TILE; ++jj) {
+              const uint16_t vb = *reinterpret_cast<const uint16_t *>(V + ap_at<D>(jj, e >> 3) + (e & 7) * 2);
+              const float v = Q4 ? f16_lo(vb) : bf16_bits_to_float(vb);
+              const bool in = (there[jj >> 5] >> (jj & 31)) & 1u;
+#pragma unroll
+              for (int k = 0; k < 16; ++k) {
+                const int c = c0 + k;
+                const bool vis = in && j0 + jj <= sh.hi[par][c] && (j0 + jj > sh.lo[par][c] || j0 + jj < a.sinks);
+                const uint16_t wb = *reinterpret_cast<const uint16_t *>(
+                    Pt + (c >> 3) * 2048 + (jj >> 6) * 1024 + (c & 7) * 128 + ((((jj >> 3) ^ c) & 7) * 16) + (jj & 7) * 2);
+                const float w = Q4 ? f16_lo(wb) : bf16_bits_to_float(wb);
+                if (vis) o[k] = __float_as_uint(fmaf(w, v, __uint_as_float(o[k])));
+              }
+            }
+            __syncwarp();
+            tmem_st_x16(tmem + lanes + O_COL + c0, o);
+          }
+          tmem_st_wait();
+          half_sync();
+        }
+        tc_fence_before_sync();
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.p_full[it & 1]);
+      }
+
+      // --- the segment's end -------------------------------------------------------
+      // Every row's sum over the warp's lanes, halves of the rows at a time: lane i
+      // ends with row i mod HC.
+#pragma unroll
+      for (int w = HC / 2; w > 0; w >>= 1) {
+        const bool up = lane & w;
+#pragma unroll
+        for (int c = 0; c < w; ++c) {
+          const float mine = up ? l[c + w] : l[c], theirs = up ? l[c] : l[c + w];
+          l[c] = mine + __shfl_xor_sync(0xffffffffu, theirs, w);
+        }
+      }
+      if (HC == 16) l[0] += __shfl_xor_sync(0xffffffffu, l[0], 16);
+      if (lane < HC) sh.part[quarter][cb + lane] = l[0];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.q_empty[par]);
+      half_sync();
+      const bool whole = seg.tile == 0 && seg.end == seg.nt;
+      float *slot = p.part + (size_t)(2 * cta + (seg.tile == 0)) * C::SLOT;
+      auto row_of = [&](int lr) {
+        const int r = seg.rt * p.RT + lr, t = per_head(r);
+        return (seg.b * T + t) * a.Hq + seg.h * p.G + r - t * p.G;
+      };
+      if (ht < HC) {
+        const int c = cb + ht;
+        const float sum = (sh.part[0][c] + sh.part[1][c]) + (sh.part[2][c] + sh.part[3][c]);
+        if (!whole)  // (maximum, sum)
+          *reinterpret_cast<float2 *>(slot + 2 * c) =
+              make_float2(sh.set[c] ? -sh.coef[c].y : -3.402823466e38f, sum);
+        sh.inv[c] = sum != 0.f ? a.v_unit / sum : -1.f;
+        sh.row[c] = row_of(c);
+      }
+      wait(&sh.pv_done[(it - 1) & 1], (it - 1) >> 1);  // (the products end in order)
+      tc_fence_after_sync();
+      half_sync();
+#pragma unroll
+      for (int cc = 0; cc < HC; cc += 16) {
+        const int c0 = cb + cc;
+        if (c0 >= n_rows) break;
+        uint32_t o[16];
+        tmem_get(tmem + lanes + O_COL + c0, o);
+        if (ht < D) {
+          if (whole) {
+            float inv[16];
+            int row[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              inv[k] = sh.inv[c0 + k];
+              row[k] = sh.row[c0 + k];
+            }
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const uint16_t v = !(inv[k] < 0.f) ? float_to_bf16_bits(__uint_as_float(o[k]) * inv[k]) : (uint16_t)0;
+              if (c0 + k < n_rows) a.out[(size_t)row[k] * D + ht] = v;
+            }
+          } else {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) slot[2 * NC + (c0 + k) * D + ht] = __uint_as_float(o[k]);
+          }
+        }
+      }
+      tc_fence_before_sync();
+      if (!whole) {
+        // CTAs ca .. cb hold tiles of the unit, ca its first; the last to arrive
+        // joins their parts, in order.
+        auto cut = [&](int x) { return cut_in(raw_cut(x), seg.unit, seg.nt); };
+        int ca = cta, cb = cta;
+        while (cut(ca) > 0) --ca;
+        while (cb + 1 < P && cut(cb + 1) < seg.nt) ++cb;
+        __threadfence();  // this thread's sums, before the count
+        named_bar_sync(6, 256);
+        if (tid == 0) {
+          const bool last = atomicAdd(p.counters + ca, 1u) == (uint32_t)(cb - ca);
+          if (last) p.counters[ca] = 0;
+          sh.joins = last;
+        }
+        named_bar_sync(6, 256);
+        if (sh.joins) {
+          __threadfence();
+          // slot 2 x + 1 of the CTA that holds the unit's first tile, 2 x of the others
+          auto of = [&](int x) { return p.part + (size_t)(2 * x + (x == ca)) * C::SLOT; };
+          constexpr int LR = D / 4;  // lanes to a row, four elements each
+          for (int c = tid / LR; c < n_rows; c += 256 / LR) {
+            const int e = 4 * (tid & (LR - 1));
+            float mj = -3.402823466e38f, lj = 0.f;
+#pragma unroll 8
+            for (int y = ca; y <= cb; ++y) mj = fmaxf(mj, __ldcg(of(y) + 2 * c));
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+            for (int y = ca; y <= cb; ++y) {
+              const float2 ml = __ldcg(reinterpret_cast<const float2 *>(of(y) + 2 * c));
+              const float4 o = __ldcg(reinterpret_cast<const float4 *>(of(y) + 2 * NC + c * D + e));
+              const float w = exp2_weight(ml.x - mj);
+              lj += ml.y * w;
+              v.x += o.x * w;
+              v.y += o.y * w;
+              v.z += o.z * w;
+              v.w += o.w * w;
+            }
+            const float w = lj != 0.f ? a.v_unit / lj : 0.f;
+            uint2 out = make_uint2(0, 0);
+            if (w != 0.f) out = make_uint2(ap_pack2<false>(v.x * w, v.y * w), ap_pack2<false>(v.z * w, v.w * w));
+            *reinterpret_cast<uint2 *>(a.out + (size_t)sh.row[c] * D + e) = out;
+          }
+        }
+      }
+      if (!next_segment(seg)) break;
+      named_bar_sync(6, 256);  // the rows' state is written again
+    }
+  } else if (warp == AW_MMA_WARP) {
+    // --- the MMAs ------------------------------------------------------------------
+    constexpr uint32_t FMT = Q4 ? 0u : 1u, BASE = (1u << 4) | (FMT << 7) | (FMT << 10) | ((uint32_t)(NC >> 3) << 17) | ((128u >> 4) << 24);
+    constexpr uint32_t ID_S = BASE, ID_O = BASE | (1u << 15);  // V^T: A along its rows
+    constexpr uint32_t STEP = C::OPERAND >> 4;
+    const uint64_t k0 = ap_desc_k_major<D>(smem_addr(smem + C::K_OFF)), q0 = ap_desc_k_major<D>(smem_addr(smem + C::Q_OFF)),
+                   p0 = ap_desc_k_major<128>(smem_addr(smem + C::P_OFF));
+    // (D = 64: what stands for elements 64 .. 127 is other positions' elements,
+    // and O^T's upper lanes are not used)
+    const uint64_t v0 = ap_desc_n_major<D>(smem_addr(smem + C::V_OFF));
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    auto scores = [&](int i, int par) {
+      if (elect_lane()) {
+        const uint64_t k = k0 + (i & 1) * STEP, q = q0 + par * (C::Q_BYTES >> 4);
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const uint32_t off = (ks >> 2) * (1024 >> 4) + (ks & 3) * 2;
+          mma_bf16_ss(tm + 64 * (i & 1), k + off, q + off, ID_S, ks > 0);
+        }
+        mma_commit(&sh.s_full[i & 1]);
+        mma_commit(&sh.k_empty[i & 1]);
+      }
+      __syncwarp();
+    };
+    // Scores are a tile ahead of the products: (sseg, sn_) is where they are.
+    Segment ss = begin(), os = ss;
+    int sn = 0, st = ss.tile, ot = os.tile;
+    bool ok = true, s_more = true;
+    auto next_scores = [&](int i) {
+      if (st == ss.tile) ok = ok && wait(&sh.q_full[sn & 1], sn >> 1);
+      ok = ok && wait(&sh.k_full[i & 1], i >> 1);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) return;
+      tc_fence_after_sync();
+      scores(i, sn & 1);
+      if (++st == ss.end) {
+        s_more = next_segment(ss);
+        ++sn;
+        st = ss.tile;
+      }
+    };
+    next_scores(0);
+    for (int i = 0; i < count && ok; ++i) {
+      if (i + 1 < count && s_more) next_scores(i + 1);
+      ok = ok && wait(&sh.v_full[i & 1], i >> 1) && wait(&sh.p_full[i & 1], i >> 1);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after_sync();
+      const bool odd = sh.odd[i & 1] != 0;
+      if (elect_lane()) {
+        if (!odd) {
+          const uint64_t v = v0 + (i & 1) * STEP, w = p0 + (i & 1) * (C::P_BYTES >> 4);
+#pragma unroll
+          for (int kk = 0; kk < AP_TILE / 16; ++kk)
+            mma_bf16_ss(tm + O_COL, v + kk * (2 * C::GROUP >> 4), w + (kk >> 2) * (1024 >> 4) + (kk & 3) * 2, ID_O,
+                        kk > 0 ? 1 : ot > os.tile);
+        }
+        mma_commit(&sh.pv_done[i & 1]);
+      }
+      __syncwarp();
+      if (++ot == os.end) {
+        next_segment(os);
+        ot = os.tile;
+      }
+    }
+    // What was issued ends before the tensor memory goes back.
+    int never = 0;
+    if (elect_lane()) mma_commit(&sh.fin);
+    __syncwarp();
+    mbar_wait_bounded(&sh.fin, 0, &never);
+  } else if (warp == AW_Q_WARP) {
+    // --- the rows' queries, a segment ahead ----------------------------------------
+    const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;  // a negative scale's sign goes into q
+    constexpr int LR = D / 8, PER = 32 / LR, N = 32 / PER;        // lanes to a row, rows at a time, loads ahead
+    const int piece = lane & (LR - 1), first = lane / LR;
+    Segment s = begin();
+    for (int n = 0;; ++n) {
+      const int par = n & 1, n_rows = rows_in(s);
+      if (n >= 2 && !__all_sync(0xffffffffu, wait(&sh.q_empty[par], (n >> 1) - 1))) break;
+      uint8_t *dst = smem + C::Q_OFF + par * C::Q_BYTES;
+      const long long p0 = (long long)__ldg(a.seq_len + s.b) + a.t0;
+#pragma unroll 1
+      for (int c0 = 0; c0 < NC; c0 += N * PER) {
+        uint4 q[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const int lr = c0 + first + i * PER;
+          q[i] = make_uint4(0, 0, 0, 0);
+          if (lr < n_rows) {
+            const int r = s.rt * p.RT + lr, t = per_head(r);
+            q[i] = __ldg(reinterpret_cast<const uint4 *>(a.y + (size_t)(s.b * T + t) * a.ld + a.q_col +
+                                                         (size_t)(s.h * p.G + r - t * p.G) * D) + piece);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          uint32_t w[4] = {q[i].x ^ flip, q[i].y ^ flip, q[i].z ^ flip, q[i].w ^ flip};
+          float m = fabsf(a.scale_log2);
+          if (Q4) {
+            // fp16 relative to the row's largest magnitude (a power of two, given
+            // back to the scores): exact but for entries 2^-14 below it.
+            uint32_t mx = 0;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mx = max(mx, max(w[k] & 0x7FFFu, (w[k] >> 16) & 0x7FFFu));
+#pragma unroll
+            for (int k = 1; k < LR; k <<= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, k));
+            const uint32_t e = min(max(mx >> 7, 1u), 253u);
+            const float down = __uint_as_float((254u - e) << 23);
+            m *= __uint_as_float(e << 23);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              w[k] = ap_pack2<true>(__uint_as_float(w[k] << 16) * down, __uint_as_float(w[k] & 0xFFFF0000u) * down);
+          }
+          const int lr = c0 + first + i * PER;
+          if (piece == 0) sh.mul[par][lr] = m;
+          *reinterpret_cast<uint4 *>(dst + ap_at<D>(lr, piece)) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+      for (int c = lane; c < NC; c += 32) {
+        const long long pos = p0 + per_head(s.rt * p.RT + c);
+        sh.hi[par][c] = c < n_rows ? (int)min(pos, 0x7ffffffell) : -1;
+        sh.lo[par][c] = a.window ? (int)max(min(pos - a.window, 0x7ffffffell), -1ll) : -1;
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.q_full[par]);
+      if (!next_segment(s)) break;
+    }
+  } else if (MODE == AP_BOXES) {
+    const int lb = p.box_log2, n_box = AP_TILE >> lb, bytes = (128 * (D / 64)) << lb;
+    const uint32_t every = n_box == 32 ? 0xffffffffu : (1u << n_box) - 1u;
+    Segment s = begin();
+    int done[2] = {0, 0};  // tiles asked for
+    const uint64_t policy = policy_evict_first();
+    bool ok = true;
+    for (int i = 0; ok; ) {
+      auto slot_of = [&](int j) {  // the box's first slot; -1: none
+        if (j >= s.end || lane >= n_box) return -1;
+        const int pos = attn_tile_start<AP_TILE>(s.r, j) + (lane << lb);
+        if (pos >= (j < s.r.st ? s.r.sink : s.r.n)) return -1;
+        const int page = p.bs_shift >= 0 ? pos >> p.bs_shift : pos / a.block_size;
+        const int blk = __ldg(a.block_table + (size_t)s.b * a.max_blocks + page);
+        if (blk < 0 || blk >= a.num_blocks) {
+          raise_status(a.status, MLORA_DEV_BAD_SLOT);
+          return -1;
+        }
+        return blk * a.block_size + pos - page * a.block_size;
+      };
+      int next = slot_of(s.tile);
+      for (int j = s.tile; j < s.end && ok; ++j, ++i) {
+        const int stage = i & 1;
+        const int slot = next;
+        next = slot_of(j + 1);
+        const uint32_t there = __ballot_sync(0xffffffffu, slot >= 0);
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+          ok = i < 2 || __all_sync(0xffffffffu, wait(v ? &sh.pv_done[stage] : &sh.k_empty[stage], (i >> 1) - 1));
+          if (!ok) break;
+          uint8_t *dst = smem + (v ? C::V_OFF : C::K_OFF) + stage * C::OPERAND;
+          if (there != every) {  // boxes that are not read are zeros
+            for (uint32_t left = every & ~there; left; left &= left - 1) {
+              uint4 *at = reinterpret_cast<uint4 *>(dst + (((__ffs(left) - 1) << lb) >> 3) * C::GROUP);
+              for (int e = lane; e < (D / 8) << lb; e += 32) at[e] = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+          }
+          if (!v && lane < AP_GROUPS) {
+            uint32_t bits = 0xffffffffu;
+            if (there != every) {
+              bits = 0;
+              for (int k = 0; k < 32; ++k) bits |= ((there >> ((32 * lane + k) >> lb)) & 1u) << k;
+            }
+            sh.there[i & 3][lane] = bits;
+          }
+          __syncwarp();
+          uint64_t *bar = v ? &sh.v_full[stage] : &sh.k_full[stage];
+          ++done[v];
+          if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(__popc(there) * bytes));
+          __syncwarp();
+          if (slot >= 0)
+            tma_load_5d(dst + ((lane << lb) >> 3) * C::GROUP, v ? &v_map : &k_map, bar, 0, 0, 0, slot >> 3, s.h, policy);
+        }
+      }
+      if (!ok || !next_segment(s)) break;
+    }
+    // The copies on their way end before the CTA does.
+    int never = 0;
+    for (int v = 0; v < 2; ++v)
+      for (int k = max(done[v] - 2, 0); k < done[v]; ++k)
+        mbar_wait_bounded(v ? &sh.v_full[k & 1] : &sh.k_full[k & 1], (k >> 1) & 1, &never);
+  } else {
+    // --- codes: of each tile a warp has 32 positions of K or of V (and so waits for
+    // every phase of its barriers).  They come to places of its own in shared
+    // memory, AHEAD tiles ahead: registers would not hold that many.
+    // Four lanes (D = 128) or two (D = 64) to a position, 16 bytes of codes each.
+    constexpr int CL = D / 32, PER = 32 / CL, NI = 32 / PER, AHEAD = AW_AHEAD, SB = D / 16;
+    const int w = warp - AW_Q_WARP - 1, cl = lane & (CL - 1), t0 = lane / CL, group = w & 3;
+    const bool values = w & 4;
+    uint8_t *raw = smem + C::RAW_OFF + w * AHEAD * C::RAW_BYTES;
+    const uint8_t *codes = static_cast<const uint8_t *>(values ? a.v : a.k) + cl * 16, *scales = values ? a.vs : a.ks;
+    Segment s = begin();
+    Seen sn = seen_of(s);
+    // A tile's pages are looked up when the one before it is asked for.
+    int blk = 0, at_h = 0, off = -1;  // page, head, offset in the page (-1: nothing to read)
+    bool at_part = false;
+    auto look_up = [&](int i) {
+      off = -1;
+      if (i >= count) return;
+      while (i >= s.i + s.end - s.tile) {
+        next_segment(s);
+        sn = seen_of(s);
+      }
+      const int j = s.tile + i - s.i, j0 = attn_tile_start<AP_TILE>(s.r, j), pos = j0 + 32 * group + lane;
+      if (pos < (j < s.r.st ? s.r.sink : s.r.n)) {
+        const int page = p.bs_shift >= 0 ? pos >> p.bs_shift : pos / a.block_size;
+        blk = __ldg(a.block_table + (size_t)s.b * a.max_blocks + page);
+        off = pos - page * a.block_size;
+      }
+      at_h = s.h;
+      at_part = partial(sn, j0);
+    };
+    uint32_t there[AHEAD];  // of the tiles on their way
+    bool part[AHEAD];
+    int put_at = 0;
+    auto fetch = [&](int i, int place) {
+      there[AHEAD - 1] = 0;
+      part[AHEAD - 1] = at_part;
+      if (i < count) {
+        int slot = -1;
+        if (off >= 0) {
+          if (blk >= 0 && blk < a.num_blocks)
+            slot = (blk * a.H + at_h) * a.block_size + off;
+          else
+            raise_status(a.status, MLORA_DEV_BAD_SLOT);
+        }
+        there[AHEAD - 1] = __ballot_sync(0xffffffffu, slot >= 0);
+        const uint32_t dst = smem_addr(raw + place * C::RAW_BYTES);
+        aw_cp_async_small<SB>(dst + 32 * (D / 2) + lane * SB, scales + (size_t)max(slot, 0) * SB, slot >= 0);
+#pragma unroll
+        for (int k = 0; k < NI; ++k) {
+          const int at = __shfl_sync(0xffffffffu, slot, k * PER + t0);
+          ap_cp_async_16(dst + k * 512 + lane * 16, codes + (size_t)max(at, 0) * (D / 2), at >= 0);
+        }
+        look_up(i + 1);
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    look_up(0);
+    for (int i = 0; i < AHEAD; ++i) {
+#pragma unroll
+      for (int k = 0; k + 1 < AHEAD; ++k) {
+        there[k] = there[k + 1];
+        part[k] = part[k + 1];
+      }
+      fetch(i, i);
+    }
+    for (int i = 0; i < count; ++i) {
+      const int stage = i & 1;
+      ap_cp_async_wait<AHEAD - 1>();
+      __syncwarp();
+      if (i >= 2 && !__all_sync(0xffffffffu, wait(values ? &sh.pv_done[stage] : &sh.k_empty[stage], (i >> 1) - 1))) break;
+      uint8_t *dst = smem + (values ? C::V_OFF : C::K_OFF) + stage * C::OPERAND;
+      const uint8_t *src = raw + put_at * C::RAW_BYTES;
+      // Pieces 4 cl .. 4 cl + 3 of the row; lanes of the upper 64 elements
+      // start two pieces later, so that eight lanes' stores differ in bank.
+      const int turn = cl & 2;
+      bool odd = false;
+#pragma unroll
+      for (int k = 0; k < NI; ++k) {
+        const uint8_t *from = src + k * 512 + lane * 16;
+        const uint2 c0 = *reinterpret_cast<const uint2 *>(from + 4 * turn), c1 = *reinterpret_cast<const uint2 *>(from + 8 - 4 * turn);
+        const uint32_t sc = *reinterpret_cast<const unsigned short *>(src + 32 * (D / 2) + (k * PER + t0) * SB + 2 * cl);
+        odd |= ((sc & 0x7Fu) == 0x7Fu) | ((sc & 0x7F00u) == 0x7F00u);
+        const uint32_t two = e4m3x2_to_f16(sc);
+        const uint32_t s01[2] = {__byte_perm(two, 0, turn ? 0x3232 : 0x1010), __byte_perm(two, 0, turn ? 0x1010 : 0x3232)};
+        const uint32_t words[4] = {c0.x, c0.y, c1.x, c1.y};
+        const int row = 32 * group + k * PER + t0;
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          uint32_t f[4];
+          e2m1x8_to_f16(words[n], f);
+          const uint32_t m = s01[n >> 1];
+          *reinterpret_cast<uint4 *>(dst + ap_at<D>(row, 4 * cl + (n ^ turn))) =
+              make_uint4(ap_hmul2(f[0], m), ap_hmul2(f[1], m), ap_hmul2(f[2], m), ap_hmul2(f[3], m));
+        }
+      }
+      odd = __any_sync(0xffffffffu, odd) && part[0];
+      if (lane == 0) {
+        if (values)
+          sh.scales[stage][group] = odd;
+        else
+          sh.there[i & 3][group] = there[0];
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(values ? &sh.v_full[stage] : &sh.k_full[stage]);
+#pragma unroll
+      for (int k = 0; k + 1 < AHEAD; ++k) {
+        there[k] = there[k + 1];
+        part[k] = part[k + 1];
+      }
+      fetch(i + AHEAD, put_at);
+      if (++put_at == AHEAD) put_at = 0;
+    }
+    ap_cp_async_wait<0>();
+  }
+  tc_fence_before_sync();
+  block_sync();
+  if (warp == AW_MMA_WARP) {
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, 256);
+  }
+  if (tid == 0 && sh.abort) raise_status(a.status, MLORA_DEV_TIMEOUT);
+}
+
+size_t attn_wide_scratch_bytes(int D, int num_sms) { return (size_t)2 * num_sms * (2 * 64 + 64 * (size_t)D) * 4; }
+
+template <int MODE, int D, int NC>
+static cudaError_t launch_wide(const AwArgs &p, const CUtensorMap &k_map, const CUtensorMap &v_map, int num_sms,
+                               cudaStream_t s) {
+  static int done[64] = {0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  constexpr int smem = AwCfg<D, NC>::smem(MODE == AP_CODES);
+  if (dev >= 64 || !done[dev]) {
+    e = cudaFuncSetAttribute(attn_wide_kernel<MODE, D, NC>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) done[dev] = 1;
+  }
+  return launch_pdl(attn_wide_kernel<MODE, D, NC>, dim3((unsigned)num_sms), dim3(aw_threads(MODE)), smem, s, p, k_map,
+                    v_map);
+}
+
+bool attn_wide_takes(const AttnArgs &a, bool q4) { return q4 || a.block_size % 8 == 0; }
+
+cudaError_t launch_attn_wide(const AttnArgs &a, bool q4, float *part, uint32_t *counters, int num_sms, cudaStream_t s) {
+  AwArgs p;
+  p.a = a;
+  p.G = a.Hq / a.H;
+  p.G_magic = (uint32_t)(((1ull << 32) + p.G - 1) / p.G);
+  const long long rq = (long long)a.rows_per_req * p.G;
+  // 64 rows at a time; 32 over the 4-bit cache, where expanding leaves too few
+  // registers for more.
+  const int most = q4 ? 32 : 64;
+  p.n_rt = (int)((rq + most - 1) / most);
+  p.RT = (int)((rq + p.n_rt - 1) / p.n_rt);
+  const long long extent = (long long)a.max_blocks * a.block_size;
+  p.extent = (int)(extent < 0x7fffff00ll ? extent : 0x7fffff00ll);
+  p.bs_shift = -1;
+  for (int i = 0; i < 31; ++i)
+    if (a.block_size == 1 << i) p.bs_shift = i;
+  p.box_log2 = 0;
+  while (p.box_log2 < 7 && a.block_size % (2 << p.box_log2) == 0) ++p.box_log2;
+  p.part = part;
+  p.counters = counters;
+  CUtensorMap km = {}, vm = {};
+  if (q4)
+    return a.D == 128 ? launch_wide<AP_CODES, 128, 32>(p, km, vm, num_sms, s)
+                      : launch_wide<AP_CODES, 64, 32>(p, km, vm, num_sms, s);
+  if (!ap_map(&km, a.k, a, 1 << p.box_log2) || !ap_map(&vm, a.v, a, 1 << p.box_log2)) return cudaErrorInvalidValue;
+  if (p.RT <= 32)
+    return a.D == 128 ? launch_wide<AP_BOXES, 128, 32>(p, km, vm, num_sms, s)
+                      : launch_wide<AP_BOXES, 64, 32>(p, km, vm, num_sms, s);
+  return a.D == 128 ? launch_wide<AP_BOXES, 128, 64>(p, km, vm, num_sms, s)
+                    : launch_wide<AP_BOXES, 64, 64>(p, km, vm, num_sms, s);
+}
+
+}  // namespace mlora

@@ -227,6 +227,9 @@ cudaError_t launch_attn_general(const AttnArgs &a, bool q4, cudaStream_t s);
 size_t attn_rows_scratch_bytes(int D, int num_sms);
 // Many rows a request, the same heads (attn_prompt.cu): no scratch.
 cudaError_t launch_attn_prompt(const AttnArgs &a, bool q4, cudaStream_t s);
+size_t attn_wide_scratch_bytes(int D, int num_sms);
+bool attn_wide_takes(const AttnArgs &a, bool q4);
+cudaError_t launch_attn_wide(const AttnArgs &a, bool q4, float *part, uint32_t *counters, int num_sms, cudaStream_t s);
 cudaError_t launch_attn_rows(const AttnArgs &a, bool q4, float *part, uint32_t *counters, int num_sms, cudaStream_t s);
 
 }  // namespace mlora
