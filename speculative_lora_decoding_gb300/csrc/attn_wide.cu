@@ -29,7 +29,12 @@ template <int D, int NC>
 struct AwCfg {
   static constexpr int GROUP = ApOperand<D>::GROUP, OPERAND = ApOperand<D>::BYTES;
   static constexpr int Q_BYTES = NC / 8 * GROUP;        // NC rows of D elements
-  static constexpr int P_BYTES = NC / 8 * ApOperand<128>::GROUP;  // NC rows of 128 positions
+  // The weights, 128 positions of NC rows each: a thread's go into one place.  A
+  // position's 2 NC bytes in pieces of 16, swizzled over the bytes' span.
+  static constexpr int P_BYTES = 256 * NC;
+  __device__ static int p_at(int pos, int piece) {
+    return 2 * NC * pos + ((piece ^ (NC == 64 ? pos : pos >> 1)) & (NC / 8 - 1)) * 16;
+  }
   static constexpr int K_OFF = 0;                       // two stages
   static constexpr int V_OFF = 2 * OPERAND;             // two stages
   static constexpr int Q_OFF = 4 * OPERAND;             // of this segment and the next
@@ -75,6 +80,18 @@ struct AwArgs {
   float *part;  // two slots per CTA
   uint32_t *counters;
 };
+
+// Weights for O^T += V^T P^T: eight positions' 2 NC bytes to a swizzle atom.
+template <int NC>
+__device__ __forceinline__ uint64_t aw_desc_p(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)(16 * NC >> 4) << 16;  // leading byte offset (one atom wide: not used)
+  d |= (uint64_t)(16 * NC >> 4) << 32;  // stride byte offset: the next eight positions
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)(NC == 64 ? 2 : 4) << 61;  // swizzles over 128 or 64 bytes
+  return d;
+}
 
 template <int BYTES>
 __device__ __forceinline__ void aw_cp_async_small(uint32_t dst, const void *src, bool there) {
@@ -427,17 +444,18 @@ __global__ void __launch_bounds__(aw_threads(MODE), 1)
           half_sync();  // what moved is written again later
         }
         if (it >= 2) wait(&sh.pv_done[it & 1], (it - 2) >> 1);  // P's place is free
-        uint8_t *P = smem + C::P_OFF + (it & 1) * C::P_BYTES + (cb >> 3) * 2048 + (ht >> 6) * 1024 + (ht & 7) * 2;
-        const uint32_t swz = (uint32_t)(ht >> 3) & 7u;
+        uint8_t *P = smem + C::P_OFF + (it & 1) * C::P_BYTES;
 #pragma unroll
-        for (int c = 0; c < HC; c += 2) {
-          const float w0 = exp2_weight(d[c]), w1 = exp2_weight(d[c + 1]);
-          l[c] += w0;
-          l[c + 1] += w1;
-          const uint32_t two = ap_pack2<Q4>(w0, w1);
-          *reinterpret_cast<uint16_t *>(P + (c >> 3) * 2048 + (c & 7) * 128 + ((swz ^ (c & 7)) * 16)) = (uint16_t)two;
-          *reinterpret_cast<uint16_t *>(P + (c >> 3) * 2048 + ((c + 1) & 7) * 128 + ((swz ^ ((c + 1) & 7)) * 16)) =
-              (uint16_t)(two >> 16);
+        for (int c = 0; c < HC; c += 8) {
+          uint32_t two[4];
+#pragma unroll
+          for (int k = 0; k < 8; k += 2) {
+            const float w0 = exp2_weight(d[c + k]), w1 = exp2_weight(d[c + k + 1]);
+            l[c + k] += w0;
+            l[c + k + 1] += w1;
+            two[k / 2] = ap_pack2<Q4>(w0, w1);
+          }
+          *reinterpret_cast<uint4 *>(P + C::p_at(ht, (cb + c) >> 3)) = make_uint4(two[0], two[1], two[2], two[3]);
         }
         bool odd = false;
         if (part) {
@@ -486,7 +504,7 @@ __global__ void __launch_bounds__(aw_threads(MODE), 1)
                 const int c = c0 + k;
                 const bool vis = in && j0 + jj <= sh.hi[par][c] && (j0 + jj > sh.lo[par][c] || j0 + jj < a.sinks);
                 const uint16_t wb = *reinterpret_cast<const uint16_t *>(
-                    Pt + (c >> 3) * 2048 + (jj >> 6) * 1024 + (c & 7) * 128 + ((((jj >> 3) ^ c) & 7) * 16) + (jj & 7) * 2);
+                    Pt + C::p_at(jj, c >> 3) + (c & 7) * 2);
                 const float w = Q4 ? f16_lo(wb) : bf16_bits_to_float(wb);
                 if (vis) o[k] = __float_as_uint(fmaf(w, v, __uint_as_float(o[k])));
               }
@@ -615,10 +633,10 @@ __global__ void __launch_bounds__(aw_threads(MODE), 1)
   } else if (warp == AW_MMA_WARP) {
     // --- the MMAs ------------------------------------------------------------------
     constexpr uint32_t FMT = Q4 ? 0u : 1u, BASE = (1u << 4) | (FMT << 7) | (FMT << 10) | ((uint32_t)(NC >> 3) << 17) | ((128u >> 4) << 24);
-    constexpr uint32_t ID_S = BASE, ID_O = BASE | (1u << 15);  // V^T: A along its rows
+    constexpr uint32_t ID_S = BASE, ID_O = BASE | (3u << 15);  // V^T and P^T: along their rows
     constexpr uint32_t STEP = C::OPERAND >> 4;
     const uint64_t k0 = ap_desc_k_major<D>(smem_addr(smem + C::K_OFF)), q0 = ap_desc_k_major<D>(smem_addr(smem + C::Q_OFF)),
-                   p0 = ap_desc_k_major<128>(smem_addr(smem + C::P_OFF));
+                   p0 = aw_desc_p<NC>(smem_addr(smem + C::P_OFF));
     // (D = 64: what stands for elements 64 .. 127 is other positions' elements,
     // and O^T's upper lanes are not used)
     const uint64_t v0 = ap_desc_n_major<D>(smem_addr(smem + C::V_OFF));
@@ -666,7 +684,7 @@ __global__ void __launch_bounds__(aw_threads(MODE), 1)
           const uint64_t v = v0 + (i & 1) * STEP, w = p0 + (i & 1) * (C::P_BYTES >> 4);
 #pragma unroll
           for (int kk = 0; kk < AP_TILE / 16; ++kk)
-            mma_bf16_ss(tm + O_COL, v + kk * (2 * C::GROUP >> 4), w + (kk >> 2) * (1024 >> 4) + (kk & 3) * 2, ID_O,
+            mma_bf16_ss(tm + O_COL, v + kk * (2 * C::GROUP >> 4), w + kk * (32 * NC >> 4), ID_O,
                         kk > 0 ? 1 : ot > os.tile);
         }
         mma_commit(&sh.pv_done[i & 1]);
