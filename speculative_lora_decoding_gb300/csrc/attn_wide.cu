@@ -21,9 +21,9 @@
 
 namespace mlora {
 
-constexpr int AW_MMA_WARP = 8, AW_Q_WARP = 9, AW_AHEAD = 3;
+constexpr int AW_MMA_WARP = 8, AW_Q_WARP = 9, AW_LOAD_WARP = 11, AW_AHEAD = 3;
 __host__ __device__ constexpr int aw_loaders(int mode) { return mode == AP_BOXES ? 1 : 8; }
-__host__ __device__ constexpr int aw_threads(int mode) { return 32 * (AW_Q_WARP + 1 + aw_loaders(mode)); }
+__host__ __device__ constexpr int aw_threads(int mode) { return 32 * (AW_LOAD_WARP + aw_loaders(mode)); }
 
 template <int D, int NC>
 struct AwCfg {
@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(aw_threads(MODE), 1)
   // --- the share ---------------------------------------------------------------
   // Units are cut up by time: a unit's start counts as START tiles.  A request's
   // tiles (of one unit) and whether it has any, in one number.
-  constexpr int START = 2, BITS = 20;
+  constexpr int START = Q4 ? 2 : 1, BITS = 20;
   auto counted = [&](int b) {
     const int nt = b < a.B ? range_of(b).nt : 0;
     return nt ? ((long long)(nt + START) << BITS) + 1 : 0ll;
@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(aw_threads(MODE), 1)
   const long long quot = total < (1ll << 31) ? (long long)((uint32_t)total / (uint32_t)P) : total / P;
   const int rest = (int)(total - quot * P);
   auto raw_cut = [&](int x) { return quot * x + (uint32_t)(rest * x) / (uint32_t)P; };
-  const int near = (int)min(quot / 16, 1ll << 20) + 1;
+  const int near = (int)min(quot / 4, (long long)START) + 1;
   // The tile of a unit that starts at `unit` and has nt tiles where CTA x's share
   // begins: 0 if before it, nt if after it; cuts near an end of the unit go there.
   auto cut_in = [&](long long raw, long long unit, int nt) {
@@ -291,7 +291,7 @@ __global__ void __launch_bounds__(aw_threads(MODE), 1)
   if (tid == 0) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&sh.q_full[i], 1);
+      mbar_init(&sh.q_full[i], AW_LOAD_WARP - AW_Q_WARP);
       mbar_init(&sh.q_empty[i], 8);
       mbar_init(&sh.k_full[i], MODE == AP_BOXES ? 1 : AP_GROUPS);
       mbar_init(&sh.v_full[i], MODE == AP_BOXES ? 1 : AP_GROUPS);
@@ -602,28 +602,45 @@ __global__ void __launch_bounds__(aw_threads(MODE), 1)
           __threadfence();
           // slot 2 x + 1 of the CTA that holds the unit's first tile, 2 x of the others
           auto of = [&](int x) { return p.part + (size_t)(2 * x + (x == ca)) * C::SLOT; };
-          constexpr int LR = D / 4;  // lanes to a row, four elements each
-          for (int c = tid / LR; c < n_rows; c += 256 / LR) {
-            const int e = 4 * (tid & (LR - 1));
-            float mj = -3.402823466e38f, lj = 0.f;
-#pragma unroll 8
-            for (int y = ca; y <= cb; ++y) mj = fmaxf(mj, __ldcg(of(y) + 2 * c));
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-            for (int y = ca; y <= cb; ++y) {
+          // 16 bytes of the result per thread and row; all rows' loads of two parts
+          // on their way at a time.
+          constexpr int LR = D / 8, PER = 256 / LR, R = (NC + PER - 1) / PER;
+          const int e = 8 * (tid & (LR - 1)), c0 = tid / LR;
+          float m[R], sum[R], v[R][8];
+#pragma unroll
+          for (int k = 0; k < R; ++k) {
+            m[k] = -3.402823466e38f;
+            sum[k] = 0.f;
+#pragma unroll
+            for (int n = 0; n < 8; ++n) v[k][n] = 0.f;
+          }
+#pragma unroll 2
+          for (int y = ca; y <= cb; ++y) {
+#pragma unroll
+            for (int k = 0; k < R; ++k) {
+              const int c = min(c0 + k * PER, NC - 1);
               const float2 ml = __ldcg(reinterpret_cast<const float2 *>(of(y) + 2 * c));
-              const float4 o = __ldcg(reinterpret_cast<const float4 *>(of(y) + 2 * NC + c * D + e));
-              const float w = exp2_weight(ml.x - mj);
-              lj += ml.y * w;
-              v.x += o.x * w;
-              v.y += o.y * w;
-              v.z += o.z * w;
-              v.w += o.w * w;
+              const float4 o0 = __ldcg(reinterpret_cast<const float4 *>(of(y) + 2 * NC + c * D + e));
+              const float4 o1 = __ldcg(reinterpret_cast<const float4 *>(of(y) + 2 * NC + c * D + e + 4));
+              const float top = fmaxf(m[k], ml.x), was = exp2_weight(m[k] - top), is = exp2_weight(ml.x - top);
+              const float o[8] = {o0.x, o0.y, o0.z, o0.w, o1.x, o1.y, o1.z, o1.w};
+              m[k] = top;
+              sum[k] = sum[k] * was + ml.y * is;
+#pragma unroll
+              for (int n = 0; n < 8; ++n) v[k][n] = v[k][n] * was + o[n] * is;
             }
-            const float w = lj != 0.f ? a.v_unit / lj : 0.f;
-            uint2 out = make_uint2(0, 0);
-            if (w != 0.f) out = make_uint2(ap_pack2<false>(v.x * w, v.y * w), ap_pack2<false>(v.z * w, v.w * w));
-            *reinterpret_cast<uint2 *>(a.out + (size_t)sh.row[c] * D + e) = out;
+          }
+#pragma unroll
+          for (int k = 0; k < R; ++k) {
+            const int c = c0 + k * PER;
+            if (c >= n_rows) break;
+            uint4 out = make_uint4(0, 0, 0, 0);
+            if (sum[k] != 0.f) {
+              const float w = a.v_unit / sum[k];
+              out = make_uint4(ap_pack2<false>(v[k][0] * w, v[k][1] * w), ap_pack2<false>(v[k][2] * w, v[k][3] * w),
+                               ap_pack2<false>(v[k][4] * w, v[k][5] * w), ap_pack2<false>(v[k][6] * w, v[k][7] * w));
+            }
+            *reinterpret_cast<uint4 *>(a.out + (size_t)sh.row[c] * D + e) = out;
           }
         }
       }
@@ -700,11 +717,11 @@ __global__ void __launch_bounds__(aw_threads(MODE), 1)
     if (elect_lane()) mma_commit(&sh.fin);
     __syncwarp();
     mbar_wait_bounded(&sh.fin, 0, &never);
-  } else if (warp == AW_Q_WARP) {
-    // --- the rows' queries, a segment ahead ----------------------------------------
+  } else if (warp < AW_LOAD_WARP) {
+    // --- the rows' queries, a segment ahead; half the rows per warp ----------------------------------------
     const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;  // a negative scale's sign goes into q
-    constexpr int LR = D / 8, PER = 32 / LR, N = 32 / PER;        // lanes to a row, rows at a time, loads ahead
-    const int piece = lane & (LR - 1), first = lane / LR;
+    constexpr int LR = D / 8, PER = 32 / LR, N = 16 / PER;        // lanes to a row, rows at a time, loads ahead
+    const int piece = lane & (LR - 1), first = (warp - AW_Q_WARP) * (NC / 2) + lane / LR;
     Segment s = begin();
     for (int n = 0;; ++n) {
       const int par = n & 1, n_rows = rows_in(s);
@@ -712,7 +729,7 @@ __global__ void __launch_bounds__(aw_threads(MODE), 1)
       uint8_t *dst = smem + C::Q_OFF + par * C::Q_BYTES;
       const long long p0 = (long long)__ldg(a.seq_len + s.b) + a.t0;
 #pragma unroll 1
-      for (int c0 = 0; c0 < NC; c0 += N * PER) {
+      for (int c0 = 0; c0 < NC / 2; c0 += N * PER) {
         uint4 q[N];
 #pragma unroll
         for (int i = 0; i < N; ++i) {
@@ -748,7 +765,7 @@ __global__ void __launch_bounds__(aw_threads(MODE), 1)
           *reinterpret_cast<uint4 *>(dst + ap_at<D>(lr, piece)) = make_uint4(w[0], w[1], w[2], w[3]);
         }
       }
-      for (int c = lane; c < NC; c += 32) {
+      for (int c = (warp - AW_Q_WARP) * 32 + lane; c < NC; c += 64) {
         const long long pos = p0 + per_head(s.rt * p.RT + c);
         sh.hi[par][c] = c < n_rows ? (int)min(pos, 0x7ffffffell) : -1;
         sh.lo[par][c] = a.window ? (int)max(min(pos - a.window, 0x7ffffffell), -1ll) : -1;
@@ -826,7 +843,7 @@ __global__ void __launch_bounds__(aw_threads(MODE), 1)
     // memory, AHEAD tiles ahead: registers would not hold that many.
     // Four lanes (D = 128) or two (D = 64) to a position, 16 bytes of codes each.
     constexpr int CL = D / 32, PER = 32 / CL, NI = 32 / PER, AHEAD = AW_AHEAD, SB = D / 16;
-    const int w = warp - AW_Q_WARP - 1, cl = lane & (CL - 1), t0 = lane / CL, group = w & 3;
+    const int w = warp - AW_LOAD_WARP, cl = lane & (CL - 1), t0 = lane / CL, group = w & 3;
     const bool values = w & 4;
     uint8_t *raw = smem + C::RAW_OFF + w * AHEAD * C::RAW_BYTES;
     const uint8_t *codes = static_cast<const uint8_t *>(values ? a.v : a.k) + cl * 16, *scales = values ? a.vs : a.ks;
