@@ -685,6 +685,46 @@ size_t mlora_attention_workspace_bytes(int M, int rows_per_req, int Hq, int H, i
   return align_up(WS_SCRATCH_OFF + (attn_head_fast(D) ? std::max(attn_rows_scratch_bytes(D, sms), attn_wide_scratch_bytes(D, sms)) : 0), 256);
 }
 
+// Which kernel takes heads of 64 and 128, by the R rows that read a cache head
+// together.  Measured for 128 requests of 2000 tokens, 8 cache heads of 128 (32
+// requests for heads of 64), in us:
+//                        R     rows  wide  prompt
+//   bf16, heads of 128   8      180   181     228
+//                       10      204   181     228
+//                       64      353   193     236
+//                       96        -   369     237
+//   bf16, heads of 64   32       49    53      58
+//                       40       67    56      58
+//   4-bit, heads of 128 16      112   150     311
+//                       20      168   149     310
+//                       64      419   278     315
+//                       96        -   404     317
+//   4-bit, heads of 64  16       35    45      58
+//                       20       52    45      59
+//                       40       78    78      60
+// The wide kernel takes 64 rows (32 over the 4-bit cache) at a time and cuts the
+// work into equal shares; the prompt kernel takes 256 at a time and a CTA per
+// unit, however long (one request of 30000 tokens, R = 256: 424 against 90 us).
+// So beside a time per tile each, which the measurements above give, what counts
+// is how many times the wide kernel goes over the cache and how full the prompt
+// kernel's last wave of CTAs is.  Past 256 rows the prompt kernel's CTAs see
+// fewer positions than all rows together.
+enum class AttnKernel { ROWS, WIDE, PROMPT };
+static AttnKernel attn_kernel(const AttnArgs &a, bool q4, int sms) {
+  const long long R = (long long)a.rows_per_req * (a.Hq / a.H);
+  if (R <= (q4 ? 16 : a.D == 128 ? 8 : 32)) return AttnKernel::ROWS;
+  if (R <= 256 && attn_wide_takes(a, q4)) {
+    const int at_a_time = q4 ? 32 : 64;
+    const long long units = (long long)((a.M + a.rows_per_req - 1) / a.rows_per_req) * a.H;
+    const long long wide = (R + at_a_time - 1) / at_a_time * units, prompt = (units + sms - 1) / sms * sms;
+    const int tile = a.D == 64 ? (q4 ? 11 : 10) : q4 ? 20 : 12;  // the prompt kernel's, in tenths of the wide one's
+    if (wide * 10 <= prompt * tile) return AttnKernel::WIDE;
+  }
+  // (Rows that the wide kernel leaves here: pages of sizes that are not a multiple
+  // of 8, and 33 or more over the 4-bit cache.)
+  return R >= 64 || (q4 && R > 32) ? AttnKernel::PROMPT : AttnKernel::ROWS;
+}
+
 static mlora_status attention_impl(const void *y, int M, int ld, int q_col, int Hq, int H, int D, const void *k,
                                    const void *v, const uint8_t *ks, const uint8_t *vs, float k_unit, float v_unit,
                                    int num_blocks, int block_size, const int32_t *block_table, int B, int max_blocks,
@@ -732,14 +772,14 @@ static mlora_status attention_impl(const void *y, int M, int ld, int q_col, int 
   if (M == 0) return MLORA_OK;
   uint8_t *ws = (uint8_t *)workspace;
   const bool fast = attn_head_fast(D) && ld % 8 == 0 && q_col % 8 == 0 && aligned(y, 16) && aligned(k, 16) && aligned(v, 16);
-  if (fast && (long long)rows_per_req * (Hq / H) >= 64) return cuda_status(launch_attn_prompt(a, q4, (cudaStream_t)stream));
-  if (fast && (long long)rows_per_req * (Hq / H) > 16 && attn_wide_takes(a, q4))
-    return cuda_status(launch_attn_wide(a, q4, reinterpret_cast<float *>(ws + WS_SCRATCH_OFF),
-                                        reinterpret_cast<uint32_t *>(ws + WS_COUNTERS_OFF), sms, (cudaStream_t)stream));
-  if (fast)
-    return cuda_status(launch_attn_rows(a, q4, reinterpret_cast<float *>(ws + WS_SCRATCH_OFF),
-                                        reinterpret_cast<uint32_t *>(ws + WS_COUNTERS_OFF), sms, (cudaStream_t)stream));
-  return cuda_status(launch_attn_general(a, q4, (cudaStream_t)stream));
+  float *scratch = reinterpret_cast<float *>(ws + WS_SCRATCH_OFF);
+  uint32_t *counters = reinterpret_cast<uint32_t *>(ws + WS_COUNTERS_OFF);
+  if (!fast) return cuda_status(launch_attn_general(a, q4, (cudaStream_t)stream));
+  switch (attn_kernel(a, q4, sms)) {
+    case AttnKernel::ROWS: return cuda_status(launch_attn_rows(a, q4, scratch, counters, sms, (cudaStream_t)stream));
+    case AttnKernel::WIDE: return cuda_status(launch_attn_wide(a, q4, scratch, counters, sms, (cudaStream_t)stream));
+    default: return cuda_status(launch_attn_prompt(a, q4, (cudaStream_t)stream));
+  }
 }
 
 mlora_status mlora_attention(const void *y, int M, int ld, int q_col, int Hq, int H, int D, const void *k_cache,
