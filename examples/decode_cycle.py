@@ -1,0 +1,170 @@
+"""Speculative multi-LoRA decoding of a small attention model, end to end.
+
+A prompt pass fills the paged cache (LoRA on); then each cycle drafts `k`
+tokens with LoRA off, verifies them and the last token in one LoRA-on pass that
+overwrites their cache slots, accepts or resamples, and commits.  Every step is
+a call of the library; PyTorch holds the memory and does the norms, residuals
+and embedding look-ups between them.
+
+    python examples/decode_cycle.py                       # bf16 cache
+    python examples/decode_cycle.py --cache q4            # the cache in 4 bits
+    python examples/decode_cycle.py --window 64 --sinks 4
+"""
+import argparse
+import os
+import sys
+import time
+
+import torch
+
+sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+
+import speculative_lora_decoding_gb300 as ml  # noqa: E402
+
+
+class Cache:
+    """One layer's K and V pages, in bf16 or in 4 bits, and what reads and writes them."""
+
+    def __init__(self, kind, num_blocks, block_size, H, D):
+        self.q4, self.H, self.D = kind == "q4", H, D
+        if self.q4:
+            shape = (num_blocks, H, block_size)
+            self.parts = [torch.zeros((*shape, n), dtype=torch.uint8, device="cuda") for n in (D // 2, D // 16) * 2]
+        else:
+            self.parts = [torch.zeros((num_blocks, block_size, H, D), dtype=torch.bfloat16, device="cuda") for _ in "kv"]
+
+    def write(self, y, Hq, table, seq, T, t0, ws):
+        at = Hq * self.D, (Hq + self.H) * self.D, self.H, self.D
+        (ml.kv_write_q4 if self.q4 else ml.kv_write)(y, *at, table, seq, T, t0, *self.parts, ws=ws)
+
+    def attention(self, y, Hq, table, seq, T, t0, window, sinks, ws):
+        fn = ml.attention_q4 if self.q4 else ml.attention
+        return fn(y, 0, Hq, *self.parts, table, seq, T, t0, window=window, sinks=sinks, ws=ws)
+
+
+class Model:
+    """Layers of norm, fused q|k|v, attention, o and a residual; tied to a vocabulary at both ends."""
+
+    def __init__(self, layers=2, hidden=512, Hq=8, H=2, D=64, vocab=2048, adapters=4, rank=16, cache="bf16",
+                 num_blocks=256, block_size=16, window=0, sinks=0, seed=0):
+        g = torch.Generator("cuda").manual_seed(seed)
+        self.Hq, self.H, self.D, self.hidden, self.vocab = Hq, H, D, hidden, vocab
+        self.window, self.sinks, self.block_size = window, sinks, block_size
+
+        def weight(*shape, by):
+            return (torch.randn(shape, generator=g, device="cuda") * by ** -0.5).to(torch.bfloat16)
+
+        def linear(n, k):  # W, and each adapter's A and B
+            return weight(n, k, by=k), weight(adapters, rank, k, by=k), weight(adapters, n, rank, by=16 * rank)
+
+        self.embed = weight(vocab, hidden, by=1)
+        self.qkv = [linear((Hq + 2 * H) * D, hidden) for _ in range(layers)]
+        self.o = [linear(hidden, Hq * D) for _ in range(layers)]
+        self.head = linear(vocab, hidden)
+        self.ranks = torch.full((adapters,), rank, dtype=torch.int32, device="cuda")
+        self.caches = [Cache(cache, num_blocks, block_size, H, D) for _ in range(layers)]
+        self.spaces = {}
+
+    def _space(self, M, T, adapters):
+        """Workspaces of a pass of M rows, kept for the next pass of this size."""
+        if (M, T) not in self.spaces:
+            sizes = [ml.linear_workspace_bytes(M, w.shape[0], w.shape[1], adapters)
+                     for w in (self.qkv[0][0], self.o[0][0], self.head[0])]
+            self.spaces[M, T] = (ml.Workspace(max(sizes)), ml.Workspace(ml.kv_workspace_bytes()),
+                                 ml.Workspace(ml.attention_workspace_bytes(M, T, self.Hq, self.H, self.D)))
+        return self.spaces[M, T]
+
+    def forward(self, tokens, adapter, table, seq, t0, mode):
+        """Logits fp32 [B, T, vocab] of tokens [B, T] at positions seq[b] + t0 + 0 .. T - 1."""
+        B, T = tokens.shape
+        lin, kv, att = self._space(B * T, T, self.ranks.numel())
+        idx = adapter.repeat_interleave(T).contiguous()
+
+        def layer(x, w):
+            return ml.linear(x, w[0], w[1], w[2], self.ranks, idx, 1.0, mode, ws=lin)
+
+        def norm(x):
+            return torch.nn.functional.rms_norm(x.float(), (self.hidden,)).to(torch.bfloat16)
+
+        x = self.embed[tokens.reshape(-1).long()].float()
+        for qkv, o, cache in zip(self.qkv, self.o, self.caches):
+            y = layer(norm(x), qkv)
+            cache.write(y, self.Hq, table, seq, T, t0, kv)
+            x = x + layer(cache.attention(y, self.Hq, table, seq, T, t0, self.window, self.sinks, att), o).float()
+        return layer(norm(x), self.head).float().view(B, T, self.vocab)
+
+    def status(self):
+        """Device status bits of all passes so far (0: nothing went wrong)."""
+        bits = 0
+        for space in self.spaces.values():
+            for ws in space:
+                bits |= ws.status()
+        return bits
+
+
+def decode(model, prompts, adapter, k, cycles, seed=0):
+    """`cycles` decode cycles after the prompts; returns each request's tokens and
+    how many drafts were accepted in all."""
+    B, g = len(prompts), torch.Generator("cuda").manual_seed(seed)
+    longest = max(len(p) for p in prompts)
+    most = longest + cycles * (k + 1) + k + 1
+    blocks = (most + model.block_size - 1) // model.block_size
+    table = torch.randperm(model.caches[0].parts[0].shape[0], generator=g, device="cuda")[:B * blocks]
+    table = table.view(B, blocks).int().contiguous()
+
+    # The prompts but for their last tokens, padded at the end: what the padding
+    # writes is past the committed lengths and written over later.
+    padded = torch.tensor([p[:-1] + [0] * (longest - len(p)) for p in prompts], device="cuda")
+    seq = torch.zeros(B, dtype=torch.int32, device="cuda")
+    if longest > 1:
+        model.forward(padded, adapter, table, seq, 0, ml.VERIFY)
+    seq = torch.tensor([len(p) - 1 for p in prompts], dtype=torch.int32, device="cuda")
+    last = torch.tensor([p[-1] for p in prompts], dtype=torch.int32, device="cuda")
+
+    out, kept = [list(p) for p in prompts], 0
+    for _ in range(cycles):
+        u = torch.rand((2 * k + 1, B), generator=g, device="cuda")
+        tokens, z_draft = [last], []
+        for t in range(k):  # LoRA off, a row per request
+            z = model.forward(tokens[-1].view(B, 1), adapter, table, seq, t, ml.DRAFT).view(B, model.vocab)
+            tokens.append(ml.draft_sample(z, u[t].contiguous(), want_q=False)[0])
+            z_draft.append(z)
+        row = torch.stack(tokens, 1)
+        z = model.forward(row, adapter, table, seq, 0, ml.VERIFY)
+        new, accepted = ml.verify_accept_logits(z, torch.stack(z_draft, 1), row[:, 1:].contiguous(),
+                                                u[k:].t().contiguous())
+        ml.kv_commit(accepted, seq)
+        last = new.gather(1, accepted.long().view(B, 1)).view(B).contiguous()
+        for b, (n, toks) in enumerate(zip(accepted.tolist(), new.tolist())):
+            out[b] += toks[:n + 1]
+            kept += n
+    return out, kept
+
+
+def main():
+    ap = argparse.ArgumentParser(description=__doc__.split("\n")[0])
+    ap.add_argument("--cache", choices=("bf16", "q4"), default="bf16")
+    ap.add_argument("--requests", type=int, default=8)
+    ap.add_argument("--drafts", type=int, default=4)
+    ap.add_argument("--cycles", type=int, default=8)
+    ap.add_argument("--window", type=int, default=0)
+    ap.add_argument("--sinks", type=int, default=0)
+    a = ap.parse_args()
+    g = torch.Generator().manual_seed(1)
+    prompts = [torch.randint(0, 2048, (5 + 7 * i,), generator=g).tolist() for i in range(a.requests)]
+    adapter = (torch.arange(a.requests, device="cuda") % 4).int()
+    longest = 5 + 7 * a.requests + (a.cycles + 1) * (a.drafts + 1)
+    model = Model(cache=a.cache, window=a.window, sinks=a.sinks, num_blocks=a.requests * (longest // 16 + 1))
+    decode(model, prompts, adapter, a.drafts, 1)  # (the first launches load the kernels)
+    torch.cuda.synchronize()
+    t = time.perf_counter()
+    out, kept = decode(model, prompts, adapter, a.drafts, a.cycles)
+    torch.cuda.synchronize()
+    t = time.perf_counter() - t
+    new = sum(len(o) - len(p) for o, p in zip(out, prompts))
+    print(f"{a.cache} cache: {new} tokens in {a.cycles} cycles of {a.requests} requests, {kept} of "
+          f"{a.cycles * a.requests * a.drafts} drafts kept, {t / a.cycles * 1e3:.2f} ms a cycle, status {model.status()}")
+
+
+if __name__ == "__main__":
+    main()
