@@ -12,9 +12,18 @@
 // Each half's tile is handed back and forth in two parts of 64 positions, so
 // that the scores of the next part are there when a thread is done with one
 // (with whole tiles, the way from P through the MMAs to the next scores stood
-// between a half's exponentials: 3600 cycles a tile against ... now).  The running maximum m moves (and O is rescaled,
-// in tensor memory) only when a score exceeds it by 8 in log2 units; until
-// then a tile is one pass over its scores.
+// between a half's exponentials).  The running maximum m moves (and O is
+// rescaled, in tensor memory) only when a score exceeds it by 8 in log2 units;
+// until then a tile is one pass over its scores.
+//
+// Measured: 2 prompts of 4000 rows, 32 heads on 8 of 128, behind up to 1500
+// positions: 335 us, 0.55 of the dense bf16 rate of a library product; 1024 rows
+// of each of 2 requests behind 4 to 7 thousand positions in 4 bits: 261 us, 0.40.
+// A tile takes 3600 cycles, of which its MMAs need 2500 (the second product's A
+// operand in tensor memory, N = 128, runs at its full rate; the first's N = 64
+// at three quarters, for which shared memory is the reason) and a part's
+// exponentials 1800 for each half at the same time: the two halves' waits for
+// each other are what is left, and 16 thousand cycles to start and end a CTA.
 //
 // Warps 0-3 and 4-7 hold the rows of the two halves, warps 8 and 9 issue their
 // MMAs (an MMA is handed over as the one before it runs, so a warp's waits would

@@ -1,5 +1,5 @@
-// Attention for few rows a request (draft steps, verify passes): heads of 64
-// and 128 on the tensor cores, over the bf16 or the 4-bit paged cache.
+// Attention for few rows a cache head (draft steps): heads of 64 and 128 on the
+// tensor cores, over the bf16 or the 4-bit paged cache.
 //
 // With R = rows x (query heads per cache head) query rows against each cache
 // head, every cached value takes part in R multiply-adds per byte or two: the
@@ -8,7 +8,7 @@
 //
 // Work.  A unit is (request, cache head, up to 32 query rows).  The tiles (16
 // or 32 positions) of all units, in order, are cut into equal contiguous
-// shares, one per warp (8 warps to a CTA, one CTA per SM), so mixed lengths
+// shares, one per warp (8 to 16 warps to a CTA, one CTA per SM), so mixed lengths
 // balance by themselves; every CTA finds its shares from the lengths on the
 // device.  A cut that would leave only a few tiles of a unit on one side
 // (less than 3 and a quarter of a share) moves to the unit's end.  A warp has its own ring of asynchronous copies,
@@ -19,7 +19,7 @@
 // the units that several CTAs share, by the last of these to arrive.
 //
 // Products.  The cache is the M side of m16n8k16 MMAs and the query rows the N
-// side, so 5 or 25 rows pad to 8 or 32 and not to 16 or 128:
+// side, so 4 or 12 rows pad to 8 or 16 and not to 16 or 128:
 //   S^T[positions, rows] = K Q^T,   O^T[D, rows] += V^T P^T.
 // P^T moves from S^T's accumulator layout to the second product's operand by
 // 8x8 register transposes.
@@ -33,6 +33,12 @@
 // the first product and of the positions in the second is free as long as
 // both operands agree, and is chosen so that a lane's 16 bytes of K codes and
 // 8 bytes of V codes are contiguous.
+//
+// Measured, in fractions of the copy bandwidth: 64 requests, one row of 32 heads
+// on 8 cache heads of 128, a window of 1000 positions and 4 sinks: 58 us, 0.67;
+// 8 requests of 20 to 66 thousand positions in 4 bits, a row of 40 heads on 8:
+// 90 us, 0.59 (expanding the codes keeps the issue slots busy); one request of
+// 700 positions: 14 us, which is launch, look-ups, one tile's loads and a join.
 #include "attn_common.cuh"
 #include "e2m1.cuh"
 
@@ -50,9 +56,9 @@ template <bool Q4, int D, int NR>
 struct ArCfg {
   static constexpr int WARPS = ar_warps(Q4, NR);
   static constexpr int THREADS = 32 * WARPS;
-  static constexpr int TILE = Q4 && NR < 3 ? 32 : 16;  // positions a warp takes at a time (16: registers)
+  static constexpr int TILE = Q4 ? 32 : 16;  // positions a warp takes at a time (as many as registers allow)
   static constexpr int MT = TILE / 16;
-  static constexpr int STAGES = Q4 ? (NR == 1 ? 2 : 96 / TILE) : 2;
+  static constexpr int STAGES = Q4 && NR > 1 ? 3 : 2;
   static constexpr int KROW = Q4 ? D / 2 : D * 2;  // bytes of a position's row
   static constexpr int SROW = Q4 ? D / 16 : 0;     // bytes of its scales
   static constexpr int V_OFF = TILE * KROW;
@@ -1098,11 +1104,13 @@ static cudaError_t launch_rows(const ArArgs &p, int num_sms, cudaStream_t s) {
 
 template <bool Q4, int D>
 static cudaError_t launch_rows_nr(const ArArgs &p, int num_sms, cudaStream_t s) {
-  switch ((p.RT + 7) / 8) {
-    case 1: return launch_rows<Q4, D, 1>(p, num_sms, s);
-    case 2: return launch_rows<Q4, D, 2>(p, num_sms, s);
-    case 3: return launch_rows<Q4, D, 3>(p, num_sms, s);
-    default: return launch_rows<Q4, D, 4>(p, num_sms, s);
+  const int nr = (p.RT + 7) / 8;
+  if (nr <= 1) return launch_rows<Q4, D, 1>(p, num_sms, s);
+  if constexpr (Q4) {
+    return launch_rows<Q4, D, 2>(p, num_sms, s);
+  } else {
+    if (nr == 2) return launch_rows<Q4, D, 2>(p, num_sms, s);
+    return nr == 3 ? launch_rows<Q4, D, 3>(p, num_sms, s) : launch_rows<Q4, D, 4>(p, num_sms, s);
   }
 }
 
@@ -1112,7 +1120,9 @@ cudaError_t launch_attn_rows(const AttnArgs &a, bool q4, float *part, uint32_t *
   p.G = a.Hq / a.H;
   p.G_magic = (uint32_t)(((1ull << 32) + p.G - 1) / p.G);
   const long long rq = (long long)a.rows_per_req * p.G;
-  p.n_rt = (int)((rq + 31) / 32);
+  // 32 rows at a time; 16 over the 4-bit cache, whose units with more go to attn_wide.cu.
+  const int most = q4 ? 16 : 32;
+  p.n_rt = (int)((rq + most - 1) / most);
   p.RT = (int)((rq + p.n_rt - 1) / p.n_rt);
   const long long extent = (long long)a.max_blocks * a.block_size;
   p.extent = (int)(extent < 0x7fffff00ll ? extent : 0x7fffff00ll);

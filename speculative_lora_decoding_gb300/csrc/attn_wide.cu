@@ -1,22 +1,33 @@
-// Attention for some tens of rows per (request, cache head) (verify passes with
-// grouped heads): heads of 64 and 128 on tcgen05, over the bf16 or the 4-bit
-// paged cache.
+// Attention for 9 to 256 rows a cache head (verify passes with grouped heads,
+// chunks of prompts over few requests): heads of 64 and 128 on tcgen05, over the
+// bf16 or the 4-bit paged cache.
 //
 // 25 query rows against a cache head are too many for the register MMAs of
-// attn_rows.cu (over the 4-bit cache those bound a pass at 3/4 of HBM before
-// anything else is counted) and too few for rows on the M side of a tcgen05
-// MMA.  Here the cache is the M side and the rows the N side:
+// attn_rows.cu (over the 4-bit cache those alone bound a pass at 3/4 of HBM) and
+// too few for rows on the M side of a tcgen05 MMA.  Here the cache is the M side
+// and the rows the N side, 32 or 64 of them:
 //   S^T[128 positions, rows] = K Q^T,   O^T[D, rows] += V^T P^T,
-// all operands in shared memory, S^T and O^T in tensor memory, so the threads
-// do one score per (position, row) and nothing else: with positions in lanes
-// every lane has work whatever the number of rows.
+// all operands in shared memory (K, Q along D; V, P along their rows), S^T and
+// O^T in tensor memory.  With positions in lanes every thread has work whatever
+// the number of rows, and a thread's weights go to shared memory in one place.
 //
-// A CTA (one per SM) has a contiguous share of all (request, head, tile)
-// triples, found on the device as in attn_rows.cu; units that cuts go through
-// are joined by the last CTA to arrive.  Warps 0-3 take the exponentials (a
-// position each), warp 4 issues the MMAs, the others bring tiles: TMA boxes, or
-// codes expanded to fp16.  The running maxima move, by whole numbers, when a
-// score exceeds its row's by 8.
+// Work.  A unit is (request, cache head, up to 64 rows, 32 over the 4-bit cache);
+// the tiles of all units are cut into equal contiguous shares, a unit's start
+// counted as a tile or two, a share per CTA (one per SM), found on the device.
+// Units that cuts go through are joined, in order, by the last CTA to arrive.
+//
+// Warps 0-7 take the exponentials, four the first half of the rows and four the
+// second: each half has its own running maxima, which move by whole numbers when
+// a score exceeds its row's by 8 in log2 units (rescaling is exact).  Warp 8
+// issues the MMAs, scores a tile ahead of the products; warps 9 and 10 bring the
+// next unit's queries; the others bring tiles: one warp as TMA boxes, or eight
+// that expand codes to fp16, exactly, from asynchronous copies three tiles ahead.
+//
+// Measured, 128 requests of 5 rows, 40 heads on 8 of 128: bf16, up to 4096
+// positions, 103 us, 0.76 of the copy bandwidth (2600 cycles a tile, which is
+// HBM; a unit's start is 2700, to first tiles from the launch 11000); 4-bit, up
+// to 8192 positions, 135 us, 0.29: 2100 to 2300 cycles a tile, in which the
+// schedulers issue 1330 instructions each, three fifths of them to expand codes.
 #include "attn_tc.cuh"
 
 namespace mlora {

@@ -221,15 +221,14 @@ struct AttnArgs {
   uint32_t *status;
 };
 cudaError_t launch_attn_general(const AttnArgs &a, bool q4, cudaStream_t s);
-// Few rows a request, heads of 64 and 128, 16-byte aligned rows
-// (attn_rows.cu): attn_rows_scratch_bytes of partial sums and one counter per
-// SM (zero between calls).
+// Heads of 64 and 128, 16-byte aligned rows.  Few rows a cache head
+// (attn_rows.cu) and up to 256 (attn_wide.cu) want their scratch_bytes of partial
+// sums and one counter per SM (zero between calls), more (attn_prompt.cu) none.
 size_t attn_rows_scratch_bytes(int D, int num_sms);
-// Many rows a request, the same heads (attn_prompt.cu): no scratch.
-cudaError_t launch_attn_prompt(const AttnArgs &a, bool q4, cudaStream_t s);
 size_t attn_wide_scratch_bytes(int D, int num_sms);
-bool attn_wide_takes(const AttnArgs &a, bool q4);
-cudaError_t launch_attn_wide(const AttnArgs &a, bool q4, float *part, uint32_t *counters, int num_sms, cudaStream_t s);
+bool attn_wide_takes(const AttnArgs &a, bool q4);  // not bf16 pages of a size that is no multiple of 8
 cudaError_t launch_attn_rows(const AttnArgs &a, bool q4, float *part, uint32_t *counters, int num_sms, cudaStream_t s);
+cudaError_t launch_attn_wide(const AttnArgs &a, bool q4, float *part, uint32_t *counters, int num_sms, cudaStream_t s);
+cudaError_t launch_attn_prompt(const AttnArgs &a, bool q4, cudaStream_t s);
 
 }  // namespace mlora
