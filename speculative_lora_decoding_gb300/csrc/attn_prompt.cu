@@ -38,21 +38,20 @@
 
 namespace mlora {
 
-constexpr int AP_MMA_WARP = 8;
-template <int D>
+template <int D, int HALVES>
 struct ApCfg {
   static constexpr int GROUP = ApOperand<D>::GROUP, OPERAND = ApOperand<D>::BYTES;
-  static constexpr int Q_OFF = 0;                       // two halves
-  static constexpr int K_OFF = 2 * OPERAND;             // two stages
-  static constexpr int V_OFF = 4 * OPERAND;             // two stages
-  static constexpr int BAR_OFF = 6 * OPERAND;
+  static constexpr int Q_OFF = 0;                       // a place per half
+  static constexpr int K_OFF = HALVES * OPERAND;        // two stages
+  static constexpr int V_OFF = K_OFF + 2 * OPERAND;     // two stages
+  static constexpr int BAR_OFF = V_OFF + 2 * OPERAND;
   static constexpr int E_OFF = BAR_OFF + 512;           // q's powers of two (4-bit cache)
-  static constexpr int SMEM = E_OFF + 2 * 128 * 4 + 1024;  // and the alignment
+  static constexpr int SMEM = E_OFF + HALVES * 128 * 4 + 1024;  // and the alignment
 };
 
 // Warps that bring tiles: with boxes one copies and one looks the tiles over.
-__host__ __device__ constexpr int ap_loaders(int mode) { return mode == AP_BOXES ? 2 : 6; }
-__host__ __device__ constexpr int ap_threads(int mode) { return 32 * (AP_MMA_WARP + 2 + ap_loaders(mode)); }
+__host__ __device__ constexpr int ap_loaders(int mode, int halves) { return mode == AP_BOXES ? 2 : 3 * halves; }
+__host__ __device__ constexpr int ap_threads(int mode, int halves) { return 32 * (5 * halves + ap_loaders(mode, halves)); }
 
 struct __align__(16) ApShared {
   uint64_t q_full, k_full[2], v_full[2], v_land[2], kv_empty[2], k0_empty, s_full[2][2], p_full[2][2], fin[2];
@@ -68,22 +67,22 @@ struct ApArgs {
   int G;
   uint32_t G_magic;
   int extent, bs_shift;
-  int n_rt, halves;  // row tiles per (request, cache head), of halves * 128 rows
-  int box_log2;      // positions of a TMA box
+  int n_rt;      // row tiles per (request, cache head)
+  int box_log2;  // positions of a TMA box
 };
 
-template <int MODE, int D>
-__global__ void __launch_bounds__(ap_threads(MODE), 1)
+template <int MODE, int D, int HALVES>
+__global__ void __launch_bounds__(ap_threads(MODE, HALVES), D == 64 && HALVES == 1 ? 2 : 1)
     attn_prompt_kernel(const ApArgs p, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
-  using C = ApCfg<D>;
+  using C = ApCfg<D, HALVES>;
   constexpr bool Q4 = MODE == AP_CODES;
-  constexpr int LOADERS = ap_loaders(MODE);
+  constexpr int LOADERS = ap_loaders(MODE, HALVES), AP_MMA_WARP = 4 * HALVES, AP_LOAD_WARP = 5 * HALVES;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = align_smem_1024(smem_raw);
   ApShared &sh = *reinterpret_cast<ApShared *>(smem + C::BAR_OFF);
   const AttnArgs &a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int T = a.rows_per_req, RT = p.halves * 128;
+  const int T = a.rows_per_req, RT = HALVES * 128;
   // Later rows see more: they go first.
   const int per = a.H * a.B;
   const int rt = p.n_rt - 1 - (int)(blockIdx.x / per);
@@ -105,12 +104,12 @@ __global__ void __launch_bounds__(ap_threads(MODE), 1)
     return a.out + ((size_t)(b * T + t) * a.Hq + h * p.G + r - t * p.G) * D;
   };
   if (nt == 0) {  // nothing to see: zeros
-    for (int i = tid; i < n_rows * (D / 8); i += ap_threads(MODE))
+    for (int i = tid; i < n_rows * (D / 8); i += ap_threads(MODE, HALVES))
       reinterpret_cast<uint4 *>(out_row(r0 + i / (D / 8)))[i % (D / 8)] = make_uint4(0, 0, 0, 0);
     return;
   }
 
-  const int halves = n_rows > 128 ? 2 : 1;
+  const int halves = HALVES == 2 && n_rows > 128 ? 2 : 1;
   if (tid == 0) {
     mbar_init(&sh.q_full, 4 * halves);
 #pragma unroll
@@ -133,7 +132,7 @@ __global__ void __launch_bounds__(ap_threads(MODE), 1)
     fence_mbar_init();
   }
   if (warp == AP_MMA_WARP) {
-    tmem_alloc(&sh.tmem, 512);
+    tmem_alloc(&sh.tmem, 256 * HALVES);
     tmem_relinquish();
   }
   tc_fence_before_sync();
@@ -150,7 +149,7 @@ __global__ void __launch_bounds__(ap_threads(MODE), 1)
     return false;
   };
   // S of half i at columns 128 i (first 64 positions of the tile) and 128 i + 64,
-  // P over each, O at 256 + 128 i.
+  // P over each, O at 128 (HALVES + i).
 
   // Whether some row of the CTA does not see all of tile j.
   const int all_below = (int)min(p_lo, 0x7ffffff0ll);  // every row sees up to here, but for its window's start
@@ -222,7 +221,7 @@ __global__ void __launch_bounds__(ap_threads(MODE), 1)
       if (lane == 0) mbar_arrive(&sh.q_full);
 
       const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-      const uint32_t ts = tmem + lanes + 128 * half, to = tmem + lanes + 256 + 128 * half;
+      const uint32_t ts = tmem + lanes + 128 * half, to = tmem + lanes + 128 * (HALVES + half);
       float m = AP_NONE, l = 0.f, mul = fabsf(a.scale_log2);
       auto rescale_o = [&](float corr) {
 #pragma unroll 1
@@ -380,7 +379,7 @@ __global__ void __launch_bounds__(ap_threads(MODE), 1)
         tc_fence_before_sync();
       }
     }
-  } else if (warp < AP_MMA_WARP + 2) {
+  } else if (warp < AP_LOAD_WARP) {
     const int half = warp - AP_MMA_WARP;
     if (half < halves) {
       // --- a half's MMAs --------------------------------------------------------
@@ -391,7 +390,7 @@ __global__ void __launch_bounds__(ap_threads(MODE), 1)
       constexpr uint32_t STEP = C::OPERAND >> 4;  // in a descriptor's address units
       const uint64_t q0 = ap_desc_k_major<D>(smem_addr(smem + C::Q_OFF)) + half * STEP,
                      k0 = ap_desc_k_major<D>(smem_addr(smem + C::K_OFF)), v0 = ap_desc_n_major<D>(smem_addr(smem + C::V_OFF));
-      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0), ts = tm + 128 * half, to = tm + 256 + 128 * half;
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0), ts = tm + 128 * half, to = tm + 128 * (HALVES + half);
       auto ready = [&](uint64_t *bar, uint32_t parity) { return mbar_try_wait(bar, parity) || wait(bar, parity); };
       // (issued by one elected lane)
       auto scores = [&](int stage, int sub) {  // 64 positions of the stage's K
@@ -451,7 +450,7 @@ __global__ void __launch_bounds__(ap_threads(MODE), 1)
       }
     }
   } else if (MODE == AP_BOXES) {
-    if (warp == AP_MMA_WARP + 2) {
+    if (warp == AP_LOAD_WARP) {
       // --- the tiles, by TMA: lane i brings the tile's box i ---------------------
       const int lb = p.box_log2, n_box = AP_TILE >> lb, bytes = (128 * (D / 64)) << lb;
       auto slot_of = [&](int j) {  // the box's first slot; -1: none
@@ -579,9 +578,9 @@ __global__ void __launch_bounds__(ap_threads(MODE), 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(x & 4 ? &sh.v_full[(x >> 3) & 1] : &sh.k_full[(x >> 3) & 1]);
     };
-    const int w = warp - AP_MMA_WARP - 2;
-    int next = slot_of(w);
+    const int w = warp - AP_LOAD_WARP;
     if (!Q4) {
+      int next = slot_of(w);
       constexpr int CH = D / 8, PER = 32 / CH;  // 16-byte pieces of a row, rows per instruction
       const int ch = lane & (CH - 1), t0 = lane / CH;
       const uint32_t stride = (uint32_t)a.H * D * 2;
@@ -649,61 +648,90 @@ __global__ void __launch_bounds__(ap_threads(MODE), 1)
         for (; done < n_groups; done += LOADERS) finish(done);
     } else {
       // Four lanes (D = 128) or two (D = 64) to a position, 16 bytes of codes
-      // (32 elements, two scales) each.
+      // (32 elements, two scales) each.  A group's codes are asked for while the
+      // one before is expanded, and its pages a group earlier.
       constexpr int CL = D / 32, PER = 32 / CL, NI = 32 / PER;
       const int cl = lane & (CL - 1), t0 = lane / CL;
-      for (int x = w; x < n_groups; x += LOADERS) {
-        const int j = x >> 3, slot = next;
-        next = slot_of(x + LOADERS);
+      struct Group {
+        uint4 q[NI];
+        uint32_t sc[NI], there;
+      };
+      int blk = 0, off = -1;  // page and offset in it (-1: nothing to read)
+      auto look_up = [&](int x) {
+        off = -1;
+        if (x >= n_groups) return;
+        const int j = x >> 3, pos = attn_tile_start<AP_TILE>(R, j) + 32 * (x & 3) + lane;
+        if (pos >= (j < R.st ? R.sink : R.n)) return;
+        const int page = p.bs_shift >= 0 ? pos >> p.bs_shift : pos / a.block_size;
+        blk = __ldg(a.block_table + (size_t)b * a.max_blocks + page);
+        off = pos - page * a.block_size;
+      };
+      auto fetch = [&](int x, Group &g) {
+        if (x >= n_groups) return;
+        int slot = -1;
+        if (off >= 0) {
+          if (blk >= 0 && blk < a.num_blocks)
+            slot = (blk * a.H + h) * a.block_size + off;
+          else
+            raise_status(a.status, MLORA_DEV_BAD_SLOT);
+        }
+        g.there = __ballot_sync(0xffffffffu, slot >= 0);
         const uint8_t *codes = static_cast<const uint8_t *>(x & 4 ? a.v : a.k) + cl * 16;
         const uint8_t *scales = (x & 4 ? a.vs : a.ks) + cl * 2;
-        uint4 q[NI];
-        uint32_t sc[NI];
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+          const int at = max(__shfl_sync(0xffffffffu, slot, i * PER + t0), 0);  // (not there: any, times zero)
+          g.q[i] = __ldg(reinterpret_cast<const uint4 *>(codes + (size_t)at * (D / 2)));
+          g.sc[i] = __ldg(reinterpret_cast<const unsigned short *>(scales + (size_t)at * (D / 16)));
+        }
+        look_up(x + LOADERS);
+      };
+      auto put = [&](int x, const Group &g) {  // false: gave up
+        const int j = x >> 3;
+        if (!room(x)) return false;
+        uint8_t *dst = smem + (x & 4 ? C::V_OFF : C::K_OFF) + (j & 1) * C::OPERAND;
         bool odd = false;
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
-          const int s = __shfl_sync(0xffffffffu, slot, i * PER + t0);
-          q[i] = make_uint4(0, 0, 0, 0);
-          sc[i] = 0;
-          if (s >= 0) {
-            q[i] = __ldg(reinterpret_cast<const uint4 *>(codes + (size_t)s * (D / 2)));
-            sc[i] = __ldg(reinterpret_cast<const unsigned short *>(scales + (size_t)s * (D / 16)));
-          }
-        }
-        if (!room(x)) break;
-        const uint32_t there = __ballot_sync(0xffffffffu, slot >= 0);
-        uint8_t *dst = smem + (x & 4 ? C::V_OFF : C::K_OFF) + (j & 1) * C::OPERAND;
-#pragma unroll
-        for (int i = 0; i < NI; ++i) {
           const int row = 32 * (x & 3) + i * PER + t0;
-          odd |= (sc[i] & 0x7Fu) == 0x7Fu || (sc[i] & 0x7F00u) == 0x7F00u;
-          const uint32_t two = e4m3x2_to_f16(sc[i]);
+          const uint32_t sc = (g.there >> (i * PER + t0)) & 1u ? g.sc[i] : 0u;
+          odd |= ((sc & 0x7Fu) == 0x7Fu) | ((sc & 0x7F00u) == 0x7F00u);
+          const uint32_t two = e4m3x2_to_f16(sc);
           const uint32_t s01[2] = {__byte_perm(two, two, 0x1010), __byte_perm(two, two, 0x3232)};
-          const uint32_t words[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+          const uint32_t words[4] = {g.q[i].x, g.q[i].y, g.q[i].z, g.q[i].w};
           uint4 o[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             uint32_t f[4];
             e2m1x8_to_f16(words[k], f);
-            const uint32_t s = s01[k >> 1];
-            o[k] = make_uint4(ap_hmul2(f[0], s), ap_hmul2(f[1], s), ap_hmul2(f[2], s), ap_hmul2(f[3], s));
+            const uint32_t m = s01[k >> 1];
+            o[k] = make_uint4(ap_hmul2(f[0], m), ap_hmul2(f[1], m), ap_hmul2(f[2], m), ap_hmul2(f[3], m));
           }
           // Pieces 4 cl .. 4 cl + 3 of the row; lanes of the upper 64 elements
           // start two pieces later, so that eight lanes' stores differ in bank.
           const bool turn = cl & 2;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
+          for (int k = 0; k < 4; ++k)
             *reinterpret_cast<uint4 *>(dst + ap_at<D>(row, 4 * cl + (turn ? k ^ 2 : k))) = turn ? o[k ^ 2] : o[k];
-          }
         }
         odd = __any_sync(0xffffffffu, odd) && partial(j);
         if (lane == 0) {
           if (x & 4)
             sh.odd[j & 1][x & 3] = odd;
           else
-            sh.there[j & 3][x & 3] = there;
+            sh.there[j & 3][x & 3] = g.there;
         }
         arrive(x);
+        return true;
+      };
+      Group g0, g1;
+      look_up(w);
+      fetch(w, g0);
+      for (int x = w; x < n_groups; x += 2 * LOADERS) {
+        fetch(x + LOADERS, g1);
+        if (!put(x, g0)) break;
+        fetch(x + 2 * LOADERS, g0);
+        if (x + LOADERS < n_groups && !put(x + LOADERS, g1)) break;
       }
     }
   }
@@ -711,25 +739,36 @@ __global__ void __launch_bounds__(ap_threads(MODE), 1)
   block_sync();
   if (warp == AP_MMA_WARP) {
     tc_fence_after_sync();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(tmem, 256 * HALVES);
   }
   if (tid == 0 && sh.abort) raise_status(a.status, MLORA_DEV_TIMEOUT);
 }
 
-template <int MODE, int D>
-static cudaError_t launch_prompt(const ApArgs &p, const CUtensorMap &k_map, const CUtensorMap &v_map, cudaStream_t s) {
+template <int MODE, int D, int HALVES>
+static cudaError_t launch_prompt_rows(const ApArgs &p, const CUtensorMap &k_map, const CUtensorMap &v_map, cudaStream_t s) {
   static int done[64] = {0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  constexpr int smem = ApCfg<D>::SMEM;
+  constexpr int smem = ApCfg<D, HALVES>::SMEM;
   if (dev >= 64 || !done[dev]) {
-    e = cudaFuncSetAttribute(attn_prompt_kernel<MODE, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    e = cudaFuncSetAttribute(attn_prompt_kernel<MODE, D, HALVES>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     if (dev < 64) done[dev] = 1;
   }
   const long long grid = (long long)p.n_rt * p.a.H * p.a.B;
-  return launch_pdl(attn_prompt_kernel<MODE, D>, dim3((unsigned)grid), dim3(ap_threads(MODE)), smem, s, p, k_map, v_map);
+  return launch_pdl(attn_prompt_kernel<MODE, D, HALVES>, dim3((unsigned)grid), dim3(ap_threads(MODE, HALVES)), smem, s, p, k_map, v_map);
+}
+
+template <int MODE, int D>
+static cudaError_t launch_prompt(ApArgs &p, const CUtensorMap &k_map, const CUtensorMap &v_map, cudaStream_t s) {
+  const long long rq = (long long)p.a.rows_per_req * p.G;
+  const int halves = D == 64 && (rq <= 128 || (MODE == AP_BOXES && p.box_log2 >= 4)) ? 1 : 2;
+  p.n_rt = (int)((rq + 128 * halves - 1) / (128 * halves));
+  if constexpr (D == 64) {
+    if (halves == 1) return launch_prompt_rows<MODE, D, 1>(p, k_map, v_map, s);
+  }
+  return launch_prompt_rows<MODE, D, 2>(p, k_map, v_map, s);
 }
 
 cudaError_t launch_attn_prompt(const AttnArgs &a, bool q4, cudaStream_t s) {
@@ -742,9 +781,6 @@ cudaError_t launch_attn_prompt(const AttnArgs &a, bool q4, cudaStream_t s) {
   p.bs_shift = -1;
   for (int i = 0; i < 31; ++i)
     if (a.block_size == 1 << i) p.bs_shift = i;
-  const long long rq = (long long)a.rows_per_req * p.G;
-  p.halves = rq > 128 ? 2 : 1;
-  p.n_rt = (int)((rq + 128 * p.halves - 1) / (128 * p.halves));
   // Boxes: the largest power of two that divides a page (and the tile).  Below
   // 8 positions a box would be less than a 1024-byte swizzle pattern.
   p.box_log2 = 0;
