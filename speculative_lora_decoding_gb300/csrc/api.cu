@@ -686,43 +686,51 @@ size_t mlora_attention_workspace_bytes(int M, int rows_per_req, int Hq, int H, i
 }
 
 // Which kernel takes heads of 64 and 128, by the R rows that read a cache head
-// together.  Measured for 128 requests of 2000 tokens, 8 cache heads of 128 (32
-// requests for heads of 64), in us:
-//                        R     rows  wide  prompt
-//   bf16, heads of 128   8      180   181     228
-//                       10      204   181     228
-//                       64      353   193     236
-//                       96        -   369     237
-//   bf16, heads of 64   32       49    53      58
-//                       40       67    56      58
-//   4-bit, heads of 128 16      112   150     311
-//                       20      168   149     310
-//                       64      419   278     315
-//                       96        -   404     317
-//   4-bit, heads of 64  16       35    45      58
-//                       20       52    45      59
-//                       40       78    78      60
+// together.  Measured for `requests` of 2000 positions (4000 for 4 to 32 requests
+// and heads of 64) and 8 cache heads, in us:
+//                      requests    R     rows  wide  prompt
+//   bf16, heads of 128      128    8      180   181     228
+//                           128   10      204   181     228
+//                           128   64      353   193     236
+//                           128   96        -   369     237
+//   bf16, heads of 64         4   32       29    23      52
+//                            64   32       74    90      68
+//                            12   64       57    45      52
+//                            32   64      125    95      64
+//   4-bit, heads of 128     128   16      112   150     296
+//                           128   20      168   149     296
+//                           128   64      419   278     296
+//                           128   96        -   404     297
+//   4-bit, heads of 64       32   16       52    74      99
+//                            32   20       85    74     100
+//                            12   64       66    59      74
+//                            32   64      149   134      99
 // The wide kernel takes 64 rows (32 over the 4-bit cache) at a time and cuts the
-// work into equal shares; the prompt kernel takes 256 at a time and a CTA per
-// unit, however long (one request of 30000 tokens, R = 256: 424 against 90 us).
-// So beside a time per tile each, which the measurements above give, what counts
-// is how many times the wide kernel goes over the cache and how full the prompt
-// kernel's last wave of CTAs is.  Past 256 rows the prompt kernel's CTAs see
+// work into equal shares; the prompt kernel takes 128 or 256 at a time and a CTA
+// per unit, however long (one request of 30000 tokens, R = 256: 424 against 90
+// us).  So what counts is how often the wide kernel goes over the cache and how
+// full the prompt kernel's waves of CTAs are, beside each one's time for a tile,
+// which the measurements above give.  Past 256 rows the prompt kernel's CTAs see
 // fewer positions than all rows together.
 enum class AttnKernel { ROWS, WIDE, PROMPT };
 static AttnKernel attn_kernel(const AttnArgs &a, bool q4, int sms) {
   const long long R = (long long)a.rows_per_req * (a.Hq / a.H);
   if (R <= (q4 ? 16 : a.D == 128 ? 8 : 32)) return AttnKernel::ROWS;
-  if (R <= 256 && attn_wide_takes(a, q4)) {
-    const int at_a_time = q4 ? 32 : 64;
-    const long long units = (long long)((a.M + a.rows_per_req - 1) / a.rows_per_req) * a.H;
-    const long long wide = (R + at_a_time - 1) / at_a_time * units, prompt = (units + sms - 1) / sms * sms;
-    const int tile = a.D == 64 ? (q4 ? 11 : 10) : q4 ? 20 : 12;  // the prompt kernel's, in tenths of the wide one's
-    if (wide * 10 <= prompt * tile) return AttnKernel::WIDE;
+  if (!attn_wide_takes(a, q4)) return R >= 64 ? AttnKernel::PROMPT : AttnKernel::ROWS;
+  if (R > 256) return AttnKernel::PROMPT;
+  const int at_a_time = q4 ? 32 : 64;
+  const long long units = (long long)((a.M + a.rows_per_req - 1) / a.rows_per_req) * a.H;
+  const long long wide = (R + at_a_time - 1) / at_a_time * units;
+  // The prompt kernel's time in tenths of the wide one's for a unit.
+  auto waves = [](long long ctas, long long at_once) { return (ctas + at_once - 1) / at_once * at_once; };
+  long long prompt;
+  if (a.D == 64 && (!q4 || R <= 128)) {  // two CTAs of 128 rows to an SM
+    const long long ctas = (R + 127) / 128 * units;
+    prompt = ctas <= sms ? sms * (q4 ? 19ll : 10ll) : waves(ctas, 2 * sms) * (q4 ? 12 : 6);
+  } else {
+    prompt = waves(units, sms) * (a.D == 64 ? 17 : q4 ? 20 : 12);
   }
-  // (Rows that the wide kernel leaves here: pages of sizes that are not a multiple
-  // of 8, and 33 or more over the 4-bit cache.)
-  return R >= 64 || (q4 && R > 32) ? AttnKernel::PROMPT : AttnKernel::ROWS;
+  return wide * 10 <= prompt ? AttnKernel::WIDE : AttnKernel::PROMPT;
 }
 
 static mlora_status attention_impl(const void *y, int M, int ld, int q_col, int Hq, int H, int D, const void *k,

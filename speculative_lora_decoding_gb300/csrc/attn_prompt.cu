@@ -763,6 +763,11 @@ static cudaError_t launch_prompt_rows(const ApArgs &p, const CUtensorMap &k_map,
 template <int MODE, int D>
 static cudaError_t launch_prompt(ApArgs &p, const CUtensorMap &k_map, const CUtensorMap &v_map, cudaStream_t s) {
   const long long rq = (long long)p.a.rows_per_req * p.G;
+  // Heads of 64: two CTAs of 128 rows fit an SM, and one's start and end go with
+  // the other's tiles (32 requests, 36 rows, 2000 positions: 37 against 58 us; 2
+  // prompts of 2000 rows: 207 against 226).  Not where bringing tiles twice as
+  // often bounds them: codes (2 prompts of 2000 rows: 312 against 244), pieces (289
+  // against 273) and boxes of 8 positions (160 against 152).
   const int halves = D == 64 && (rq <= 128 || (MODE == AP_BOXES && p.box_log2 >= 4)) ? 1 : 2;
   p.n_rt = (int)((rq + 128 * halves - 1) / (128 * halves));
   if constexpr (D == 64) {
