@@ -117,6 +117,7 @@ _SIGNATURES = {
 }
 
 _lib = None
+_Tensor = torch.Tensor
 
 
 class MLoraError(RuntimeError):
@@ -156,12 +157,24 @@ def _check(status: int, where: str):
         raise MLoraError(status, where)
 
 
+# The current stream's handle without a Stream object, which takes 3 us to make:
+# a fifth of a small call.
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream=None) -> int:
-    s = torch.cuda.current_stream() if stream is None else stream
-    return s.cuda_stream
+    if stream is None:
+        if _current_raw_stream is not None and _current_device is not None:
+            return _current_raw_stream(_current_device())
+        stream = torch.cuda.current_stream()
+    return stream.cuda_stream
 
 
 def _need(t: torch.Tensor, name: str, dtype, dim=None):
+    if (isinstance(t, _Tensor) and t.dtype is dtype and t.is_cuda and t.is_contiguous()
+            and (dim is None or t.dim() == dim)):
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
@@ -219,13 +232,14 @@ class Workspace:
             raise ValueError("workspace size must be positive (sizes outside the supported range give 0)")
         self.nbytes = int(nbytes)
         self.buf = torch.empty(self.nbytes, dtype=torch.uint8, device=device or "cuda")
+        self._ptr = self.buf.data_ptr()
         _check(_load().mlora_workspace_init(self.buf.data_ptr(), self.nbytes, _stream(stream)), "workspace_init")
         # The zeroing is asynchronous on `stream`; calls may come on any stream.
         (torch.cuda.current_stream(self.buf.device) if stream is None else stream).synchronize()
 
     @property
     def ptr(self) -> int:
-        return self.buf.data_ptr()
+        return self._ptr
 
     def status(self, clear: bool = True, stream=None) -> int:
         """Device status bits (synchronises the stream)."""
@@ -502,9 +516,9 @@ def _q4_cache(k_codes, k_scales, v_codes, v_scales):
     """Shape checks of a 4-bit cache: (num_blocks, H, block_size, D) and the four pointers."""
     nb, H, bs, half = k_codes.shape
     D = 2 * half
-    if tuple(v_codes.shape) != (nb, H, bs, half) or D % 16 != 0:
+    if v_codes.shape != (nb, H, bs, half) or D % 16 != 0:
         raise ValueError("k_codes and v_codes must both be [num_blocks, H, block_size, D/2], D a multiple of 16")
-    if tuple(k_scales.shape) != (nb, H, bs, D // 16) or tuple(v_scales.shape) != (nb, H, bs, D // 16):
+    if k_scales.shape != (nb, H, bs, D // 16) or v_scales.shape != (nb, H, bs, D // 16):
         raise ValueError("k_scales and v_scales must both be [num_blocks, H, block_size, D/16]")
     return nb, H, bs, D, [_need(t, n, torch.uint8, 4) for t, n in ((k_codes, "k_codes"), (k_scales, "k_scales"),
                                                                    (v_codes, "v_codes"), (v_scales, "v_scales"))]
@@ -551,7 +565,7 @@ def kv_read_q4(k_codes: torch.Tensor, k_scales: torch.Tensor, v_codes: torch.Ten
         k = torch.empty((B, rows, H, D), dtype=torch.bfloat16, device=k_codes.device)
     if v is None:
         v = torch.empty((B, rows, H, D), dtype=torch.bfloat16, device=k_codes.device)
-    if tuple(k.shape) != (B, rows, H, D) or tuple(v.shape) != (B, rows, H, D):
+    if k.shape != (B, rows, H, D) or v.shape != (B, rows, H, D):
         raise ValueError("k and v must be [B, rows, H, D]")
     st = _load().mlora_kv_read_q4(*ptrs, float(k_unit), float(v_unit), H, D,
                                   _need(block_table, "block_table", torch.int32, 2), B, max_blocks,
@@ -576,7 +590,7 @@ def _attention_common(y, q_col, Hq, H, D, block_table, seq_len, rows_per_req, sc
         ws = Workspace(attention_workspace_bytes(M, rows_per_req, Hq, H, D), device=y.device, stream=stream)
     if out is None:
         out = torch.empty((M, Hq * D), dtype=torch.bfloat16, device=y.device)
-    if tuple(out.shape) != (M, Hq * D):
+    if out.shape != (M, Hq * D):
         raise ValueError("out must be [M, Hq * D]")
     return float(scale), ws, out
 
@@ -594,7 +608,7 @@ def attention(y: torch.Tensor, q_col: int, Hq: int, k_cache: torch.Tensor, v_cac
     M, ld = y.shape
     B, max_blocks = block_table.shape
     nb, bs, H, D = k_cache.shape
-    if tuple(v_cache.shape) != (nb, bs, H, D):
+    if v_cache.shape != (nb, bs, H, D):
         raise ValueError("k_cache and v_cache must both be [num_blocks, block_size, H, D]")
     scale, ws, out = _attention_common(y, q_col, Hq, H, D, block_table, seq_len, rows_per_req, scale, ws, out, stream)
     st = _load().mlora_attention(_need(y, "y", torch.bfloat16, 2), M, ld, int(q_col), int(Hq), H, D,
