@@ -74,8 +74,7 @@ struct ArCfg {
   static constexpr int QMUL_OFF = Q_OFF + WARPS * QBYTES;
   static constexpr int M_OFF = QMUL_OFF + WARPS * ROWS * 4;      // [2 WARPS][ROWS]
   static constexpr int L_OFF = M_OFF + 2 * WARPS * ROWS * 4;
-  static constexpr int X_OFF = L_OFF + 2 * WARPS * ROWS * 4;        // [2 WARPS][ROWS]
-  static constexpr int MASK_OFF = X_OFF + 2 * WARPS * ROWS * 4;     // [WARPS][STAGES]
+  static constexpr int MASK_OFF = L_OFF + 2 * WARPS * ROWS * 4;     // [WARPS][STAGES]
   static constexpr int MISC_OFF = MASK_OFF + WARPS * STAGES * 4;
   static constexpr int SMEM = MISC_OFF + 2048;
 };
@@ -229,7 +228,6 @@ __global__ void __launch_bounds__(ArCfg<Q4, D, NR>::THREADS, 1) attn_rows_kernel
   float *qmul = reinterpret_cast<float *>(smem + C::QMUL_OFF) + warp * C::ROWS;
   float *sm_m = reinterpret_cast<float *>(smem + C::M_OFF);
   float *sm_l = reinterpret_cast<float *>(smem + C::L_OFF);
-  float *sm_x = reinterpret_cast<float *>(smem + C::X_OFF);
   uint32_t *vmask = reinterpret_cast<uint32_t *>(smem + C::MASK_OFF);
   ArShared &sh = *reinterpret_cast<ArShared *>(smem + C::MISC_OFF);
   const uint32_t ring = smem_addr(smem) + warp * C::RING;
@@ -266,29 +264,43 @@ __global__ void __launch_bounds__(ArCfg<Q4, D, NR>::THREADS, 1) attn_rows_kernel
     }
   };
 
-  // All tiles, the CTAs among which they are cut, and this CTA's cuts.
+  // All tiles, the CTAs among which they are cut, and this CTA's cuts.  Up to 32
+  // requests every warp finds its own, a lane to a request, and waits for no other.
+  const bool few = a.B <= 32;
   long long total = 0;
   int used = 0;  // requests with tiles
-  const int nt0 = tid < a.B ? range_of(tid).nt : 0;
-  for (int base = 0; base < a.B; base += THREADS) {
+  const int nt0 = (few ? lane : tid) < a.B ? range_of(few ? lane : tid).nt : 0;
+  if (lane < 2) sh.piece[2 * warp + lane].g0 = -1;
+  long long upto = nt0;  // (few) tiles of one unit each, up to the lane's request
+  if (few) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long u = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += u;
+    }
+    total = __shfl_sync(0xffffffffu, upto, 31);
+    used = __popc(__ballot_sync(0xffffffffu, nt0 > 0));
+  }
+  for (int base = 0; !few && base < a.B; base += THREADS) {
     long long v = base == 0 ? nt0 : base + tid < a.B ? range_of(base + tid).nt : 0;
     used += __popc(__ballot_sync(0xffffffffu, v > 0));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     total += v;
   }
-  if (lane == 0) {
-    sh.sums[warp] = total;
-    sh.used[warp] = used;
-  }
-  if (tid < 2 * WARPS) sh.piece[tid].g0 = -1;
-  __syncthreads();
-  total = 0;
-  used = 0;
+  if (!few) {
+    if (lane == 0) {
+      sh.sums[warp] = total;
+      sh.used[warp] = used;
+    }
+    __syncthreads();
+    total = 0;
+    used = 0;
 #pragma unroll
-  for (int w = 0; w < WARPS; ++w) {
-    total += sh.sums[w];
-    used += sh.used[w];
+    for (int w = 0; w < WARPS; ++w) {
+      total += sh.sums[w];
+      used += sh.used[w];
+    }
   }
   total *= U;
   // A CTA per unit while they are few and short: a unit that one CTA holds
@@ -310,8 +322,36 @@ __global__ void __launch_bounds__(ArCfg<Q4, D, NR>::THREADS, 1) attn_rows_kernel
     if (o < near || nt - o < near) return 2 * o < nt ? 0 : nt;
     return o;
   };
+  // The cut at `raw`, which is in request b, whose first unit's tiles start at
+  // start * U and which has nt tiles a unit; `at` < 0: where it is alone.
+  auto place = [&](int at, long long raw, int b, long long start, int nt) {
+    const long long in = raw - start * U;
+    const int u = in < (1ll << 31) ? (int)((uint32_t)in / (uint32_t)nt) : (int)(in / nt);
+    const int o = snap((int)(in - (long long)u * nt), nt);
+    if (at >= 0) {
+      sh.at_b[at] = b;
+      sh.at_u[at] = u;
+      sh.at_tile[at] = o;
+    }
+    return start * U + (long long)u * nt + o;
+  };
+  long long cuts[2];  // the warp's share
   long long *ends = reinterpret_cast<long long *>(smem);  // per request: tiles (of one unit each) up to its end
-  {
+  if (few) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const long long raw = raw_cut(cta * WARPS + warp + e);
+      const int x = min(__popc(__ballot_sync(0xffffffffu, upto * U <= raw)), 31);  // the first request that ends past it
+      const long long start = __shfl_sync(0xffffffffu, upto - nt0, x);
+      const int nt = __shfl_sync(0xffffffffu, nt0, x);
+      cuts[e] = raw == total ? total : place(e == 0 && lane == 0 ? warp : -1, raw, x, start, nt);
+    }
+    if (lane == 0) {
+      sh.bound[warp] = cuts[0];
+      if (warp == WARPS - 1) sh.bound[WARPS] = cuts[1];
+    }
+    __syncwarp();
+  } else {
     long long before = 0;
     for (int base = 0; base < a.B; base += THREADS) {
       __syncthreads();  // sums are written again
@@ -341,22 +381,17 @@ __global__ void __launch_bounds__(ArCfg<Q4, D, NR>::THREADS, 1) attn_rows_kernel
           for (int step = THREADS > 256 ? 256 : THREADS > 128 ? 128 : 64; step > 0; step >>= 1)
             if (x + step <= THREADS && ends[x + step - 1] * U <= raw) x += step;
           const long long start = x > 0 ? ends[x - 1] : before;
-          const int nt = (int)(ends[x] - start);
-          const long long in = raw - start * U;
-          const int u = in < (1ll << 31) ? (int)((uint32_t)in / (uint32_t)nt) : (int)(in / nt);
-          const int o = snap((int)(in - (long long)u * nt), nt);
-          sh.at_b[tid] = base + x;
-          sh.at_u[tid] = u;
-          sh.at_tile[tid] = o;
-          sh.bound[tid] = start * U + (long long)u * nt + o;
+          sh.bound[tid] = place(tid, raw, base + x, start, (int)(ends[x] - start));
         }
       }
       before = all;
     }
     __syncthreads();
+    cuts[0] = sh.bound[warp];
+    cuts[1] = sh.bound[warp + 1];
   }
-  const long long s0 = sh.bound[warp];
-  const int count = (int)(sh.bound[warp + 1] - s0);
+  const long long s0 = cuts[0];
+  const int count = (int)(cuts[1] - s0);
 
   auto advance = [&](ArCursor &x, int k) {
     x.i += k;
@@ -940,26 +975,6 @@ __global__ void __launch_bounds__(ArCfg<Q4, D, NR>::THREADS, 1) attn_rows_kernel
     const uint32_t later = firsts & ~((2u << i) - 1u);
     return parts & ~((1u << i) - 1u) & (later ? (later & (0u - later)) - 1u : 0xffffffffu);
   };
-  // Every piece's weight and the unit's maximum and sum, a row per lane.
-  {
-    int turn = 0;
-    for (uint32_t left = firsts; left; left &= left - 1, ++turn) {
-      if (turn % WARPS != warp || lane >= C::ROWS) continue;
-      const int i = __ffs(left) - 1;
-      const uint32_t mine = pieces_of(i);
-      float m = AR_EMPTY, l = 0.f;
-      for (uint32_t k = mine; k; k &= k - 1) m = fmaxf(m, sm_m[(__ffs(k) - 1) * C::ROWS + lane]);
-      for (uint32_t k = mine; k; k &= k - 1) {
-        const int at = (__ffs(k) - 1) * C::ROWS + lane;
-        const float w = exp2_weight(sm_m[at] - m);
-        l += sm_l[at] * w;
-        sm_m[at] = w;
-      }
-      sm_l[i * C::ROWS + lane] = l;
-      sm_x[i * C::ROWS + lane] = m;
-    }
-  }
-  __syncthreads();
   // Items (unit, 8 rows, 32 elements of D) go to the warps in turn.
   int shared0 = 0, shared1 = 0, n_shared = 0;  // units that other CTAs have tiles of: their first pieces
   {
@@ -980,34 +995,67 @@ __global__ void __launch_bounds__(ArCfg<Q4, D, NR>::THREADS, 1) attn_rows_kernel
       }
       for (; item < NR * MI / 2; item += WARPS) {
         const int n = item % NR, mi = item / NR * 2, at = 8 * n + 2 * c;
+        // The pieces' maxima and sums of the lane's two rows, pieces k = g (mod 8)
+        // in each lane: the unit's maximum and sum, and each piece's weight.
+        constexpr int PL = (2 * WARPS + 7) / 8;
+        float2 m = make_float2(AR_EMPTY, AR_EMPTY), l = make_float2(0.f, 0.f), w[PL];
+#pragma unroll
+        for (int q = 0; q < PL; ++q) {
+          const int k = 8 * q + g;
+          w[q] = (mine >> k) & 1u ? *reinterpret_cast<const float2 *>(sm_m + k * C::ROWS + at) : make_float2(AR_EMPTY, AR_EMPTY);
+          m.x = fmaxf(m.x, w[q].x);
+          m.y = fmaxf(m.y, w[q].y);
+        }
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) {
+          m.x = fmaxf(m.x, __shfl_xor_sync(0xffffffffu, m.x, x));
+          m.y = fmaxf(m.y, __shfl_xor_sync(0xffffffffu, m.y, x));
+        }
+#pragma unroll
+        for (int q = 0; q < PL; ++q) {
+          const int k = 8 * q + g;
+          w[q] = make_float2(exp2_weight(w[q].x - m.x), exp2_weight(w[q].y - m.y));
+          if ((mine >> k) & 1u) {
+            const float2 part = *reinterpret_cast<const float2 *>(sm_l + k * C::ROWS + at);
+            l.x += part.x * w[q].x;
+            l.y += part.y * w[q].y;
+          }
+        }
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) {
+          l.x += __shfl_xor_sync(0xffffffffu, l.x, x);
+          l.y += __shfl_xor_sync(0xffffffffu, l.y, x);
+        }
         float v[2][4];
 #pragma unroll
         for (int x = 0; x < 2; ++x)
 #pragma unroll
           for (int k = 0; k < 4; ++k) v[x][k] = 0.f;
-#pragma unroll 2
-        for (uint32_t left_k = mine; left_k; left_k &= left_k - 1) {
-          const int k = __ffs(left_k) - 1;
-          const float4 *src = (k & 1) ? reinterpret_cast<const float4 *>(smem + (k >> 1) * C::RING)
-                                      : reinterpret_cast<const float4 *>(
-                                            p.part + (size_t)(cta * WARPS + (k >> 1)) * AR_SLOT<D> + 64);
-          const float2 w = *reinterpret_cast<const float2 *>(sm_m + k * C::ROWS + at);
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const float4 y = src[((mi + x) * NR + n) * 32 + lane];
-            v[x][0] += y.x * w.x;
-            v[x][1] += y.y * w.y;
-            v[x][2] += y.z * w.x;
-            v[x][3] += y.w * w.y;
+        for (int q = 0; q < PL; ++q) {
+#pragma unroll 2
+          for (uint32_t left_k = (mine >> (8 * q)) & 0xFFu; left_k; left_k &= left_k - 1) {
+            const int kq = __ffs(left_k) - 1, k = 8 * q + kq;
+            const float4 *src = (k & 1) ? reinterpret_cast<const float4 *>(smem + (k >> 1) * C::RING)
+                                        : reinterpret_cast<const float4 *>(
+                                              p.part + (size_t)(cta * WARPS + (k >> 1)) * AR_SLOT<D> + 64);
+            const float w0 = __shfl_sync(0xffffffffu, w[q].x, 4 * kq + c), w1 = __shfl_sync(0xffffffffu, w[q].y, 4 * kq + c);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const float4 y = src[((mi + x) * NR + n) * 32 + lane];
+              v[x][0] += y.x * w0;
+              v[x][1] += y.y * w1;
+              v[x][2] += y.z * w0;
+              v[x][3] += y.w * w1;
+            }
           }
         }
-        const float2 l = *reinterpret_cast<const float2 *>(sm_l + i * C::ROWS + at);
         if (here) {
-          const float w[2] = {weight(l.x), weight(l.y)};
+          const float whole[2] = {weight(l.x), weight(l.y)};
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) v[x][k] = scaled(v[x][k], w[k & 1]);
+            for (int k = 0; k < 4; ++k) v[x][k] = scaled(v[x][k], whole[k & 1]);
             write_frag(v[x], mi + x, n, u.b, u.h, u.rt, n_rows);
           }
         } else {
@@ -1015,10 +1063,7 @@ __global__ void __launch_bounds__(ArCfg<Q4, D, NR>::THREADS, 1) attn_rows_kernel
           for (int x = 0; x < 2; ++x)
             reinterpret_cast<float4 *>(slot + 64)[((mi + x) * NR + n) * 32 + lane] =
                 make_float4(v[x][0], v[x][1], v[x][2], v[x][3]);
-          if (mi == 0 && g == 0) {
-            const float2 m = *reinterpret_cast<const float2 *>(sm_x + i * C::ROWS + at);
-            *reinterpret_cast<float4 *>(slot + 2 * at) = make_float4(m.x, l.x, m.y, l.y);
-          }
+          if (mi == 0 && g == 0) *reinterpret_cast<float4 *>(slot + 2 * at) = make_float4(m.x, l.x, m.y, l.y);
         }
       }
       item -= NR * MI / 2;
