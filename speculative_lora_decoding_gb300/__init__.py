@@ -516,12 +516,13 @@ def _q4_cache(k_codes, k_scales, v_codes, v_scales):
     """Shape checks of a 4-bit cache: (num_blocks, H, block_size, D) and the four pointers."""
     nb, H, bs, half = k_codes.shape
     D = 2 * half
-    if v_codes.shape != (nb, H, bs, half) or D % 16 != 0:
+    if v_codes.shape != k_codes.shape or D % 16 != 0:
         raise ValueError("k_codes and v_codes must both be [num_blocks, H, block_size, D/2], D a multiple of 16")
-    if k_scales.shape != (nb, H, bs, D // 16) or v_scales.shape != (nb, H, bs, D // 16):
+    scales = (nb, H, bs, D // 16)
+    if k_scales.shape != scales or v_scales.shape != scales:
         raise ValueError("k_scales and v_scales must both be [num_blocks, H, block_size, D/16]")
-    return nb, H, bs, D, [_need(t, n, torch.uint8, 4) for t, n in ((k_codes, "k_codes"), (k_scales, "k_scales"),
-                                                                   (v_codes, "v_codes"), (v_scales, "v_scales"))]
+    return nb, H, bs, D, (_need(k_codes, "k_codes", torch.uint8, 4), _need(k_scales, "k_scales", torch.uint8, 4),
+                          _need(v_codes, "v_codes", torch.uint8, 4), _need(v_scales, "v_scales", torch.uint8, 4))
 
 
 def kv_write_q4(y: torch.Tensor, k_col: int, v_col: int, H: int, D: int, block_table: torch.Tensor,
