@@ -8,7 +8,7 @@ import pytest
 import torch
 
 from tests.gpu_util import needs_gpu
-from tests.test_gpu_attention import BAD_SLOT, Case, both
+from tests.test_gpu_attention import BAD_SLOT, Case, _tolerance, both
 
 pytestmark = pytest.mark.gpu
 
@@ -144,3 +144,18 @@ def test_negative_scale_and_large_and_small_queries(q4):
     c.check(ml, scale=-0.1)
     c.y = (c.y.float() * 2.0 ** -40).to(torch.bfloat16)
     c.check(ml, scale=2.0 ** 36)
+
+
+@both
+@pytest.mark.parametrize("T,G,D,M", [(5, 5, 128, 11), (5, 5, 64, 14), (8, 8, 64, 17), (40, 4, 128, 82), (40, 4, 64, 121),
+                                     (300, 2, 128, 700), (300, 2, 64, 601), (3, 2, 128, 4), (5, 5, 128, 5)])
+def test_a_last_request_in_part_and_requests_without_rows(q4, T, G, D, M):
+    """M rows that end within a request: its first rows alone; later requests have none."""
+    ml = needs_gpu()
+    c = Case(q4, [130, 300, 77, 500], T, 2 * G, 2, D, 16, seed=M)
+    ws = ml.Workspace(ml.attention_workspace_bytes(M, T, 2 * G, 2, D))
+    got = c.device().call(ml, y=c.y_d[:M].contiguous(), ws=ws).double().cpu().numpy().reshape(M, 2 * G, D)
+    c.y = c.y[:M]
+    o, st, bound = c.oracle()
+    assert st == 0 and ws.status() == 0
+    assert (np.abs(got - o) <= _tolerance(o, bound, D, q4)).all()
