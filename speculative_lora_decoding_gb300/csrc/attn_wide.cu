@@ -158,19 +158,33 @@ __global__ void __launch_bounds__(aw_threads(MODE), 1)
     const int nt = b < a.B ? range_of(b).nt : 0;
     return nt ? ((long long)(nt + START) << BITS) + 1 : 0ll;
   };
+  // Up to 32 requests every warp finds the share by itself, a lane to a request,
+  // and waits for no other.
+  const bool few = a.B <= 32;
   long long total = 0;
-  const long long mine = counted(tid);
-  for (int base = 0; base < a.B; base += THREADS) {
+  const long long mine = counted(few ? lane : tid);
+  long long upto = mine;  // (few) up to the lane's request
+  if (few) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long u = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += u;
+    }
+    total = __shfl_sync(0xffffffffu, upto, 31);
+  }
+  for (int base = 0; !few && base < a.B; base += THREADS) {
     long long v = base == 0 ? mine : counted(base + tid);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     total += v;
   }
-  if (lane == 0) sh.sums[warp] = total;
-  __syncthreads();
-  total = 0;
+  if (!few) {
+    if (lane == 0) sh.sums[warp] = total;
+    __syncthreads();
+    total = 0;
 #pragma unroll
-  for (int w = 0; w < WARPS; ++w) total += sh.sums[w];
+    for (int w = 0; w < WARPS; ++w) total += sh.sums[w];
+  }
   const int used = (int)(total & ((1 << BITS) - 1));
   total = (total >> BITS) * U;
   // A CTA per unit while they are few and short (4 tiles).
@@ -190,8 +204,35 @@ __global__ void __launch_bounds__(aw_threads(MODE), 1)
     if (o < near || nt - o < near) return 2 * o < nt ? 0 : nt;
     return o;
   };
+  // The cut at `raw`, in request b, before which `start` is counted and whose own
+  // count follows it: where it is (kept for at >= 0), in tiles.
+  auto place = [&](int at, long long raw, int b, long long start, long long own) {
+    const int n = (int)(((start + own) >> BITS) - (start >> BITS)), nt = n - START;
+    const long long unit0 = (start >> BITS) * U, in = raw - unit0;
+    const int u = in < (1ll << 31) ? (int)((uint32_t)in / (uint32_t)n) : (int)(in / n);
+    const long long unit = unit0 + (long long)u * n;
+    const int o = cut_in(raw, unit, nt);
+    if (at >= 0) {
+      sh.at_b[at] = b;
+      sh.at_u[at] = u;
+      sh.at_tile[at] = o;
+      sh.at_unit[at] = unit;
+    }
+    // (less what the units up to this one count more)
+    return unit - START * ((start & ((1 << BITS) - 1)) * U + u) + o;
+  };
+  const long long tiles = total - (long long)used * U * START;
+  long long cuts[2];
   long long *ends = reinterpret_cast<long long *>(smem);  // the sums of `counted` up to a request
-  {
+  if (few) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const long long raw = raw_cut(cta + e);
+      const int x = min(__popc(__ballot_sync(0xffffffffu, (upto >> BITS) * U <= raw)), 31);  // the first that ends past it
+      const long long start = __shfl_sync(0xffffffffu, upto - mine, x), own = __shfl_sync(0xffffffffu, mine, x);
+      cuts[e] = raw == total ? tiles : place(tid == 0 && e == 0 ? 0 : -1, raw, x, start, own);
+    }
+  } else {
     long long before = 0;
     for (int base = 0; base < a.B; base += THREADS) {
       __syncthreads();
@@ -214,31 +255,23 @@ __global__ void __launch_bounds__(aw_threads(MODE), 1)
       if (tid < 2) {
         const long long raw = raw_cut(cta + tid);
         if (raw == total) {
-          sh.bound[tid] = total - (long long)used * U * START;
+          sh.bound[tid] = tiles;
         } else if ((before >> BITS) * U <= raw && raw < (all >> BITS) * U) {
           int x = 0;  // the first request that ends past the cut
 #pragma unroll
           for (int step = 512; step > 0; step >>= 1)
             if (x + step <= THREADS && (ends[x + step - 1] >> BITS) * U <= raw) x += step;
           const long long start = x > 0 ? ends[x - 1] : before;
-          const int n = (int)((ends[x] >> BITS) - (start >> BITS)), nt = n - START;
-          const long long unit0 = (start >> BITS) * U, in = raw - unit0;
-          const int u = in < (1ll << 31) ? (int)((uint32_t)in / (uint32_t)n) : (int)(in / n);
-          const long long unit = unit0 + (long long)u * n;
-          const int o = cut_in(raw, unit, nt);
-          sh.at_b[tid] = base + x;
-          sh.at_u[tid] = u;
-          sh.at_tile[tid] = o;
-          sh.at_unit[tid] = unit;
-          // (in tiles: less what the units up to this one count more)
-          sh.bound[tid] = unit - START * ((start & ((1 << BITS) - 1)) * U + u) + o;
+          sh.bound[tid] = place(tid, raw, base + x, start, ends[x] - start);
         }
       }
       before = all;
     }
     __syncthreads();
+    cuts[0] = sh.bound[0];
+    cuts[1] = sh.bound[1];
   }
-  const int count = (int)(sh.bound[1] - sh.bound[0]);
+  const int count = (int)(cuts[1] - cuts[0]);
   if (count == 0) return;
 
   struct Segment {
