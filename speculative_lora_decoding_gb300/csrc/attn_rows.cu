@@ -37,8 +37,8 @@
 // Measured, in fractions of the copy bandwidth: 64 requests, one row of 32 heads
 // on 8 cache heads of 128, a window of 1000 positions and 4 sinks: 58 us, 0.67;
 // 8 requests of 20 to 66 thousand positions in 4 bits, a row of 40 heads on 8:
-// 90 us, 0.59 (expanding the codes keeps the issue slots busy); one request of
-// 700 positions: 14 us, which is launch, look-ups, one tile's loads and a join.
+// 89 us, 0.60 (expanding the codes keeps the issue slots busy); one request of
+// 700 positions: 11 us, which is launch, look-ups, a warp's four tiles and a join.
 #include "attn_common.cuh"
 #include "e2m1.cuh"
 
