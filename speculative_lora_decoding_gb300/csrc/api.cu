@@ -710,27 +710,37 @@ size_t mlora_attention_workspace_bytes(int M, int rows_per_req, int Hq, int H, i
 // per unit, however long (one request of 30000 tokens, R = 256: 424 against 90
 // us).  So what counts is how often the wide kernel goes over the cache and how
 // full the prompt kernel's waves of CTAs are, beside each one's time for a tile,
-// which the measurements above give.  Past 256 rows the prompt kernel's CTAs see
-// fewer positions than all rows together.
+// which the measurements above give.  The few-rows kernel stands in for the wide
+// one where pages are not a multiple of 8 positions (1 request of 30000, R = 136:
+// 457 against 125 us; 128 of 2000, R = 40: 242 against 321).
+//
+// That holds for more rows, too (1 request of 60000 positions and 1 cache head, 500
+// rows of 8 heads: 817 against 256 us; 4 of 4000 and 8, 128 rows of 4 heads: 72
+// against 95), but where the rows span more positions than a tile or two the
+// prompt kernel's CTAs see fewer of them than all rows together: half at worst,
+// and with a window any part.
 enum class AttnKernel { ROWS, WIDE, PROMPT };
 static AttnKernel attn_kernel(const AttnArgs &a, bool q4, int sms) {
   const long long R = (long long)a.rows_per_req * (a.Hq / a.H);
   if (R <= (q4 ? 16 : a.D == 128 ? 8 : 32)) return AttnKernel::ROWS;
-  if (!attn_wide_takes(a, q4)) return R >= 64 ? AttnKernel::PROMPT : AttnKernel::ROWS;
-  if (R > 256) return AttnKernel::PROMPT;
-  const int at_a_time = q4 ? 32 : 64;
+  const bool takes = attn_wide_takes(a, q4);
   const long long units = (long long)((a.M + a.rows_per_req - 1) / a.rows_per_req) * a.H;
-  const long long wide = (R + at_a_time - 1) / at_a_time * units;
-  // The prompt kernel's time in tenths of the wide one's for a unit.
+  // Times in tenths of the wide kernel's for a unit.
+  const int at_a_time = q4 || !takes ? 32 : 64;
+  long long cut = (R + at_a_time - 1) / at_a_time * units * (takes ? 10 : a.D == 64 ? 9 : 11);
+  if (a.rows_per_req > 256) {
+    if (a.window) return AttnKernel::PROMPT;
+    cut *= 2;
+  }
   auto waves = [](long long ctas, long long at_once) { return (ctas + at_once - 1) / at_once * at_once; };
   long long prompt;
   if (a.D == 64 && (!q4 || R <= 128)) {  // two CTAs of 128 rows to an SM
     const long long ctas = (R + 127) / 128 * units;
     prompt = ctas <= sms ? sms * (q4 ? 19ll : 10ll) : waves(ctas, 2 * sms) * (q4 ? 12 : 6);
   } else {
-    prompt = waves(units, sms) * (a.D == 64 ? 17 : q4 ? 20 : 12);
+    prompt = waves((R + 255) / 256 * units, sms) * (a.D == 64 ? 17 : q4 ? 20 : 12);
   }
-  return wide * 10 <= prompt ? AttnKernel::WIDE : AttnKernel::PROMPT;
+  return cut > prompt ? AttnKernel::PROMPT : takes ? AttnKernel::WIDE : AttnKernel::ROWS;
 }
 
 static mlora_status attention_impl(const void *y, int M, int ld, int q_col, int Hq, int H, int D, const void *k,

@@ -3,7 +3,8 @@
 //
 // With hundreds of query rows against each cache head the work is 4 D
 // multiply-adds per (row, position) and the bound is the tensor cores.  A CTA
-// takes (request, cache head, 256 query rows): rows are (step, query head of
+// takes (request, cache head, 256 query rows, or 128 with heads of 64, two CTAs an
+// SM): rows are (step, query head of
 // the group) in order, so the heads that share a cache head share its tiles.
 // For each tile of 128 positions and each half of 128 rows
 //   S = Q K^T          operands in shared memory, S in tensor memory;
@@ -18,7 +19,7 @@
 //
 // Measured: 2 prompts of 4000 rows, 32 heads on 8 of 128, behind up to 1500
 // positions: 335 us, 0.55 of the dense bf16 rate of a library product; 1024 rows
-// of each of 2 requests behind 4 to 7 thousand positions in 4 bits: 261 us, 0.40.
+// of each of 2 requests behind 4 to 7 thousand positions in 4 bits: 263 us, 0.40.
 // A tile takes 3600 cycles, of which its MMAs need 2500 (the second product's A
 // operand in tensor memory, N = 128, runs at its full rate; the first's N = 64
 // at three quarters, for which shared memory is the reason) and a part's

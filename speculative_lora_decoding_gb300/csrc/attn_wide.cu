@@ -1,5 +1,5 @@
-// Attention for 9 to 256 rows a cache head (verify passes with grouped heads,
-// chunks of prompts over few requests): heads of 64 and 128 on tcgen05, over the
+// Attention for tens of rows a cache head (verify passes with grouped heads), and
+// for more over few requests (chunks of prompts behind long contexts): heads of 64 and 128 on tcgen05, over the
 // bf16 or the 4-bit paged cache.
 //
 // 25 query rows against a cache head are too many for the register MMAs of

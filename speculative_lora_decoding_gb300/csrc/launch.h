@@ -222,8 +222,9 @@ struct AttnArgs {
 };
 cudaError_t launch_attn_general(const AttnArgs &a, bool q4, cudaStream_t s);
 // Heads of 64 and 128, 16-byte aligned rows.  Few rows a cache head
-// (attn_rows.cu) and up to 256 (attn_wide.cu) want their scratch_bytes of partial
-// sums and one counter per SM (zero between calls), more (attn_prompt.cu) none.
+// (attn_rows.cu) and more (attn_wide.cu) want their scratch_bytes of partial sums and
+// one counter per SM (zero between calls), enough to fill the GPU (attn_prompt.cu)
+// none.
 size_t attn_rows_scratch_bytes(int D, int num_sms);
 size_t attn_wide_scratch_bytes(int D, int num_sms);
 bool attn_wide_takes(const AttnArgs &a, bool q4);  // not bf16 pages of a size that is no multiple of 8
